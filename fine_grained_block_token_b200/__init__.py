@@ -12,6 +12,12 @@ nvfp4)" page: one fp32 scale per activation row and per weight row.
 ``quant_act_static`` is the static activation scheme (one given scale), and
 ``grouped_linear_ue8m0`` the grouped (MoE expert) form of the UE8M0 linear.
 
+Around the linears: ``route`` (top-k choice of experts with the counts and
+the balance loss) and ``route_backward``, ``group_rows`` (rows sorted by expert
+or adapter), ``combine_rows`` (the experts' rows weighted and summed per
+token) and ``combine_rows_backward``, and ``lora_add`` (low-rank adapters of
+many requests on top of a linear's output).
+
 The functions below come from ``_binding`` (a ctypes binding of
 ``libfp8bl.so``), loaded on first use so that the ``build`` submodule can be
 imported before the library exists.  Using any of them without the library
@@ -22,7 +28,9 @@ __all__ = [
     "block_linear_fused", "block_linear_noalloc", "workspace_bytes", "fused_workspace_bytes",
     "check", "version", "quant_act_ue8m0", "quant_weight_ue8m0", "block_linear_ue8m0",
     "ue8m0_workspace_bytes", "quant_rowwise", "linear_rowwise", "quant_act_static",
-    "grouped_linear_ue8m0", "grouped_ue8m0_workspace_bytes",
+    "grouped_linear_ue8m0", "grouped_ue8m0_workspace_bytes", "route", "route_backward",
+    "route_workspace_bytes", "group_rows", "group_rows_workspace_bytes", "combine_rows",
+    "combine_rows_backward", "lora_add", "lora_add_workspace_bytes",
 ]
 
 

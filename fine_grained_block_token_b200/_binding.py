@@ -25,7 +25,9 @@ __all__ = [
     "check", "version", "quant_act_ue8m0", "quant_weight_ue8m0", "block_linear_ue8m0",
     "ue8m0_workspace_bytes",
     "quant_rowwise", "linear_rowwise", "quant_act_static", "grouped_linear_ue8m0",
-    "grouped_ue8m0_workspace_bytes",
+    "grouped_ue8m0_workspace_bytes", "route", "route_backward", "route_workspace_bytes",
+    "group_rows", "group_rows_workspace_bytes", "combine_rows", "combine_rows_backward",
+    "lora_add", "lora_add_workspace_bytes",
 ]
 
 BLOCK = 128
@@ -61,6 +63,20 @@ _lib.fp8_grouped_linear_ue8m0_ws.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64,
 _lib.fp8_grouped_linear_ue8m0_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64]
 _lib.fp8_grouped_linear_ue8m0_workspace_bytes.restype = _sz
 _lib.fp8_linear_rowwise.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp]
+_int, _f32 = ctypes.c_int, ctypes.c_float
+_lib.fp8bl_route.argtypes = [_vp, _int, _i64, _i64, _i64, _int, _int, _f32, _f32, _vp, _vp, _vp, _vp, _vp,
+                             _vp, _vp, _sz, _vp]
+_lib.fp8bl_route_backward.argtypes = [_vp, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _f32,
+                                      _vp, _vp]
+_lib.fp8bl_group_rows.argtypes = [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.fp8bl_combine_rows.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp]
+_lib.fp8bl_combine_rows_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp]
+_lib.fp8bl_lora_add.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp,
+                                _sz, _vp]
+for _f, _n in (("fp8bl_route_workspace_bytes", 2), ("fp8bl_group_rows_workspace_bytes", 2),
+               ("fp8bl_lora_add_workspace_bytes", 5)):
+    getattr(_lib, _f).argtypes = [_i64] * _n
+    getattr(_lib, _f).restype = _sz
 _lib.fp8bl_check.argtypes = [_vp]
 _lib.fp8bl_status_string.argtypes = [ctypes.c_int]
 _lib.fp8bl_status_string.restype = ctypes.c_char_p
@@ -70,7 +86,8 @@ for _f in ("fp8_quant_act", "fp8_quant_weight", "fp8_block_linear", "fp8_block_l
            "fp8_quant_weight_ue8m0", "fp8_block_linear_ue8m0", "fp8_block_linear_ue8m0_ws",
            "fp8_quant_rowwise",
            "fp8_linear_rowwise", "fp8_quant_act_static", "fp8_grouped_linear_ue8m0",
-           "fp8_grouped_linear_ue8m0_ws"):
+           "fp8_grouped_linear_ue8m0_ws", "fp8bl_route", "fp8bl_route_backward", "fp8bl_group_rows",
+           "fp8bl_combine_rows", "fp8bl_combine_rows_backward", "fp8bl_lora_add"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 STATUS = {0: "FP8BL_OK", 1: "FP8BL_ERR_NULL", 2: "FP8BL_ERR_SHAPE", 3: "FP8BL_ERR_ALIGN",
@@ -360,6 +377,188 @@ def linear_rowwise(q_a, s_a, q_w, s_w, y=None) -> torch.Tensor:
     _ok(_lib.fp8_linear_rowwise(_ptr(q_a), _ptr(s_a), _ptr(q_w), _ptr(s_w), _ptr(y), M, N, K,
                                 _stream(q_a)), "fp8_linear_rowwise")
     return y
+
+
+# Rows of several experts or adapters: the router, the sort by group, the
+# weighted sum back to the tokens, and low-rank adapters.
+_I32 = (torch.int32,)
+_LOGITS = {torch.bfloat16: 0, torch.float32: 1}
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def _out(t, name: str, dtype, shape, device) -> torch.Tensor:
+    """A given output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, (dtype,), shape, device)
+    return t
+
+
+def _route_options(logits, scoring: str):
+    dev = _device_of(logits, "logits")
+    T, E = _dims2(logits, "logits")
+    _need(logits, "logits", tuple(_LOGITS), (T, E), dev)
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
+    return dev, T, E, _LOGITS[logits.dtype], _SCORING[scoring]
+
+
+def route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+          balance: float = 0.0, mask=None, ids=None, weights=None, counts=None, loss=None, loss_grad=None,
+          workspace=None):
+    """Router of an expert layer: (bf16 or fp32) logits [T, E] -> (ids int32
+    [T, top_k], weights fp32 [T, top_k], counts int32 [E], loss fp32 [1],
+    loss_grad fp32 [E]).
+
+    ids are the experts of the largest logits (ties to the lowest index; -1
+    where only -inf is left), weights their scores times `scale`, divided by
+    their sum if `renormalize`.  counts are the tokens per expert, loss the
+    balance loss `balance * E * sum_e (counts_e / (top_k n)) * mean_t share_te`
+    over the n rows that take part, and loss_grad its slope, which
+    route_backward takes.  `mask` (bool [T]) leaves rows out.  Outputs and
+    workspace (uint8, route_workspace_bytes(T, E)) may be given."""
+    dev, T, E, kind, score = _route_options(logits, scoring)
+    if mask is not None:
+        _need(mask, "mask", (torch.bool, torch.uint8), (T,), dev)
+    ids = _out(ids, "ids", torch.int32, (T, top_k), dev)
+    weights = _out(weights, "weights", torch.float32, (T, top_k), dev)
+    counts = _out(counts, "counts", torch.int32, (E,), dev)
+    loss = _out(loss, "loss", torch.float32, (1,), dev)
+    loss_grad = _out(loss_grad, "loss_grad", torch.float32, (E,), dev)
+    ws, wsb = _workspace(route_workspace_bytes(T, E), dev, workspace)
+    _ok(_lib.fp8bl_route(_ptr(logits), kind, T, E, top_k, score, renormalize, scale, balance, _ptr(mask),
+                         _ptr(ids), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(loss_grad), _ptr(ws), wsb,
+                         _stream(logits)), "fp8bl_route")
+    return ids, weights, counts, loss, loss_grad
+
+
+def route_workspace_bytes(T: int, E: int) -> int:
+    """Workspace bytes fp8bl_route needs for these sizes."""
+    return int(_lib.fp8bl_route_workspace_bytes(T, E))
+
+
+def route_backward(logits, ids, d_weights=None, loss_grad=None, d_loss=None, scoring: str = "softmax",
+                   renormalize: bool = True, scale: float = 1.0, d_logits=None) -> torch.Tensor:
+    """Gradient of `(d_weights * weights).sum() + d_loss * loss` with respect
+    to the logits, from route()'s logits, ids and loss_grad and the same
+    options.  d_weights None: nothing through the weights; loss_grad None:
+    nothing through the loss; d_loss (fp32 [1]) None: 1."""
+    dev, T, E, kind, score = _route_options(logits, scoring)
+    k = _dims2(ids, "ids")[1]
+    _need(ids, "ids", _I32, (T, k), dev)
+    if d_weights is not None:
+        _need(d_weights, "d_weights", _F32, (T, k), dev)
+    if loss_grad is not None:
+        _need(loss_grad, "loss_grad", _F32, (E,), dev)
+    if d_loss is not None:
+        _need(d_loss, "d_loss", _F32, (1,), dev)
+    d_logits = _out(d_logits, "d_logits", logits.dtype, (T, E), dev)
+    _ok(_lib.fp8bl_route_backward(_ptr(logits), kind, _ptr(ids), _ptr(d_weights), _ptr(loss_grad),
+                                  _ptr(d_loss), T, E, k, score, renormalize, scale, _ptr(d_logits),
+                                  _stream(logits)), "fp8bl_route_backward")
+    return d_logits
+
+
+def group_rows(ids, groups: int, offsets=None, order=None, slot=None, workspace=None):
+    """Sorts entries by group: int32 ids (any shape, n in all) -> (offsets int32
+    [groups + 1], order int32 [n], slot int32 like ids).  Sorted rows
+    [offsets[g], offsets[g + 1]) are the entries of group g in their order,
+    entries with an id outside [0, groups) follow behind; slot is each entry's
+    sorted row, -1 without a group.  offsets are the expert_offsets of
+    grouped_linear_ue8m0; offsets and order are what lora_add takes."""
+    dev = _device_of(ids, "ids")
+    _need(ids, "ids", _I32, None, dev)
+    n = ids.numel()
+    offsets = _out(offsets, "offsets", torch.int32, (groups + 1,), dev)
+    order = _out(order, "order", torch.int32, (n,), dev)
+    slot = _out(slot, "slot", torch.int32, ids.shape, dev)
+    ws, wsb = _workspace(group_rows_workspace_bytes(n, groups), dev, workspace)
+    _ok(_lib.fp8bl_group_rows(_ptr(ids), n, groups, _ptr(offsets), _ptr(order), _ptr(slot), _ptr(ws), wsb,
+                              _stream(ids)), "fp8bl_group_rows")
+    return offsets, order, slot
+
+
+def group_rows_workspace_bytes(n: int, groups: int) -> int:
+    """Workspace bytes fp8bl_group_rows needs for these sizes."""
+    return int(_lib.fp8bl_group_rows_workspace_bytes(n, groups))
+
+
+def _check_combine(y, weights, slot, name: str, t):
+    dev = _device_of(y, "y")
+    n, H = _dims2(y, "y")
+    T, k = _dims2(slot, "slot")
+    _need(y, "y", _BF16, (n, H), dev)
+    _need(slot, "slot", _I32, (T, k), dev)
+    _need(weights, "weights", _F32, (T, k), dev)
+    if t is not None:
+        _need(t, name, _BF16, (T, H), dev)
+    return dev, T, n, k, H
+
+
+def combine_rows(y, weights, slot, base=None, out=None) -> torch.Tensor:
+    """out[t] = base[t] + sum_j weights[t, j] * y[slot[t, j]]: the experts'
+    rows (bf16 [n, H], sorted by expert) back to their tokens (bf16 [T, H]);
+    weights fp32 [T, k] from route, slot int32 [T, k] from group_rows (-1:
+    nothing).  `base` (bf16 [T, H]) may be `out` itself."""
+    dev, T, n, k, H = _check_combine(y, weights, slot, "base", base)
+    out = _out(out, "out", torch.bfloat16, (T, H), dev)
+    _ok(_lib.fp8bl_combine_rows(_ptr(y), _ptr(weights), _ptr(slot), _ptr(base), _ptr(out), T, n, k, H,
+                                _stream(y)), "fp8bl_combine_rows")
+    return out
+
+
+def combine_rows_backward(d_out, y, weights, slot, offsets, d_y=None, d_weights=None):
+    """Gradients of combine_rows from d_out (bf16 [T, H]): (d_y bf16 [n, H],
+    d_weights fp32 [T, k]).  `offsets` from group_rows: rows of d_y from
+    offsets[-1] on are zeros.  (The gradient of `base` is d_out.)"""
+    dev, T, n, k, H = _check_combine(y, weights, slot, "d_out", d_out)
+    if d_out is None:
+        raise TypeError("d_out must be a torch.Tensor")
+    _need(offsets, "offsets", _I32, None, dev)
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError(f"offsets must be group_rows' [groups + 1], got shape {tuple(offsets.shape)}")
+    d_y = _out(d_y, "d_y", torch.bfloat16, (n, H), dev)
+    d_weights = _out(d_weights, "d_weights", torch.float32, (T, k), dev)
+    _ok(_lib.fp8bl_combine_rows_backward(_ptr(d_out), _ptr(y), _ptr(weights), _ptr(slot),
+                                         _ptr(offsets) + 4 * (offsets.numel() - 1), _ptr(d_y),
+                                         _ptr(d_weights), T, n, k, H, _stream(y)),
+        "fp8bl_combine_rows_backward")
+    return d_y, d_weights
+
+
+def lora_add(y, x, a, b, offsets, order, scales=None, out=None, workspace=None) -> torch.Tensor:
+    """Low-rank adapters of many requests on top of a projection's output:
+    out[i] = y[i] + scales[l] * (x[i] a[l]^T) b[l]^T for the rows i of adapter l
+    (x bf16 [M, K], a [L, R, K], b [L, N, R], y [M, N]).  offsets and order come
+    from group_rows(adapter of each row, L), once per batch; rows without an
+    adapter keep y.  scales fp32 [L] or None (ones).  `out` may be `y` itself
+    (a new tensor by default); workspace as lora_add_workspace_bytes."""
+    dev = _device_of(x, "x")
+    M, K = _dims2(x, "x")
+    if not isinstance(a, torch.Tensor) or not isinstance(b, torch.Tensor):
+        raise TypeError("a and b must be torch.Tensors")
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError(f"a must be [L, R, K] and b [L, N, R], got {tuple(a.shape)} and {tuple(b.shape)}")
+    L, R, _ = a.shape
+    N = b.shape[1]
+    _need(x, "x", _BF16, (M, K), dev)
+    _need(a, "a", _BF16, (L, R, K), dev)
+    _need(b, "b", _BF16, (L, N, R), dev)
+    _need(y, "y", _BF16, (M, N), dev)
+    _need(offsets, "offsets", _I32, (L + 1,), dev)
+    _need(order, "order", _I32, (M,), dev)
+    if scales is not None:
+        _need(scales, "scales", _F32, (L,), dev)
+    out = _out(out, "out", torch.bfloat16, (M, N), dev)
+    ws, wsb = _workspace(lora_add_workspace_bytes(M, N, K, R, L), dev, workspace)
+    _ok(_lib.fp8bl_lora_add(_ptr(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(offsets), _ptr(order), _ptr(y),
+                            _ptr(out), M, N, K, R, L, _ptr(ws), wsb, _stream(x)), "fp8bl_lora_add")
+    return out
+
+
+def lora_add_workspace_bytes(M: int, N: int, K: int, R: int, L: int) -> int:
+    """Workspace bytes fp8bl_lora_add needs for these sizes."""
+    return int(_lib.fp8bl_lora_add_workspace_bytes(M, N, K, R, L))
 
 
 def workspace_bytes(M: int, N: int, K: int) -> int:

@@ -1,6 +1,7 @@
 // C-ABI entry points of libfp8bl (declared in include/fp8bl.h): argument
 // validation on the host, schedule choice, launch on the caller's stream,
 // and status reporting.  No call allocates device memory.
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <cuda_runtime.h>
@@ -80,7 +81,7 @@ const char* fp8bl_status_string(fp8bl_status s) {
   switch (s) {
     case FP8BL_OK: return "ok";
     case FP8BL_ERR_NULL: return "a required pointer is NULL";
-    case FP8BL_ERR_SHAPE: return "invalid sizes (need K, N multiples of 128, within limits)";
+    case FP8BL_ERR_SHAPE: return "invalid sizes or options for this call (see its limits)";
     case FP8BL_ERR_ALIGN: return "pointer not 16-byte aligned (4-byte for fp32 scales)";
     case FP8BL_ERR_ARCH: return "current device is not compute capability 10.0 (sm_100)";
     case FP8BL_ERR_CUDA: return "CUDA call failed";
@@ -430,6 +431,229 @@ fp8bl_status fp8_linear_rowwise(const void* q_a, const float* s_a, const void* q
   if (st != FP8BL_OK) return st;
   return from_cuda(
       launch_linear_rowwise(q_a, s_a, q_w, s_w, y_bf16, M, N, K, *d, as_cuda(stream)));
+}
+
+static size_t sz(int64_t a, int64_t b) { return static_cast<size_t>(a) * static_cast<size_t>(b); }
+
+static bool route_dims_ok(int64_t T, int64_t E, int64_t k) {
+  return dim_ok(T, true) && E >= 1 && E <= kMaxExperts && k >= 1 && k <= kMaxTopK && k <= E;
+}
+
+static bool route_options_ok(int type, int scoring, float scale) {
+  return (type == FP8BL_BF16 || type == FP8BL_F32) &&
+         (scoring == FP8BL_SOFTMAX || scoring == FP8BL_SIGMOID) && std::isfinite(scale);
+}
+
+size_t fp8bl_route_workspace_bytes(int64_t T, int64_t E) {
+  if (!route_dims_ok(T, E, 1)) return 0;
+  const DeviceInfo* d = device_info();
+  return route_workspace_bytes(T, E, d ? d->sm_count : 148);
+}
+
+fp8bl_status fp8bl_route(const void* logits, int logits_type, int64_t T, int64_t E, int64_t k,
+                         int scoring, int renormalize, float scale, float balance,
+                         const uint8_t* mask, int32_t* ids, float* weights, int32_t* counts,
+                         float* loss, float* loss_grad, void* workspace, size_t workspace_bytes,
+                         fp8bl_stream_t stream) {
+  if (!route_dims_ok(T, E, k) || !route_options_ok(logits_type, scoring, scale) ||
+      !std::isfinite(balance))
+    return FP8BL_ERR_SHAPE;
+  if (!counts || (T > 0 && (!logits || !ids || !weights))) return FP8BL_ERR_NULL;
+  if (!aligned(logits, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(counts, 4) ||
+      !aligned(loss, 4) || !aligned(loss_grad, 4) || !aligned(workspace, 16))
+    return FP8BL_ERR_ALIGN;
+  const size_t elem = logits_type == FP8BL_F32 ? 4 : 2;
+  struct {
+    const void* p;
+    size_t n;
+  } buf[] = {{logits, sz(T, E) * elem}, {mask, mask ? sz(T, 1) : 0},
+             {ids, sz(T, k) * 4},       {weights, sz(T, k) * 4},
+             {counts, sz(E, 4)},        {loss, loss ? size_t{4} : 0},
+             {loss_grad, loss_grad ? sz(E, 4) : 0}};
+  for (int o = 2; o < 7; ++o)
+    for (int i = 0; i < o; ++i)
+      if (overlap(buf[o].p, buf[o].n, buf[i].p, buf[i].n)) return FP8BL_ERR_OVERLAP;
+  const DeviceInfo* d = nullptr;
+  fp8bl_status st = current_device(&d);
+  if (st != FP8BL_OK) return st;
+  const size_t need = route_workspace_bytes(T, E, d->sm_count);
+  if (need > 0) {
+    if (!workspace) return FP8BL_ERR_NULL;
+    if (workspace_bytes < need) return FP8BL_ERR_WORKSPACE;
+    for (const auto& b : buf)
+      if (overlap(workspace, need, b.p, b.n)) return FP8BL_ERR_OVERLAP;
+  }
+  return from_cuda(launch_route(logits, logits_type == FP8BL_F32, T, E, k,
+                                scoring == FP8BL_SIGMOID, renormalize != 0, scale, balance, mask,
+                                ids, weights, counts, loss, loss_grad, workspace, d->sm_count,
+                                as_cuda(stream)));
+}
+
+fp8bl_status fp8bl_route_backward(const void* logits, int logits_type, const int32_t* ids,
+                                  const float* d_weights, const float* loss_grad,
+                                  const float* d_loss, int64_t T, int64_t E, int64_t k,
+                                  int scoring, int renormalize, float scale, void* d_logits,
+                                  fp8bl_stream_t stream) {
+  if (!route_dims_ok(T, E, k) || !route_options_ok(logits_type, scoring, scale))
+    return FP8BL_ERR_SHAPE;
+  if (T == 0) return FP8BL_OK;
+  if (!logits || !ids || !d_logits) return FP8BL_ERR_NULL;
+  if (!aligned(logits, 16) || !aligned(d_logits, 16) || !aligned(ids, 4) ||
+      !aligned(d_weights, 4) || !aligned(loss_grad, 4) || !aligned(d_loss, 4))
+    return FP8BL_ERR_ALIGN;
+  const size_t nz = sz(T, E) * (logits_type == FP8BL_F32 ? 4 : 2), nk = sz(T, k) * 4;
+  if (overlap(d_logits, nz, logits, nz) || overlap(d_logits, nz, ids, nk) ||
+      overlap(d_logits, nz, d_weights, d_weights ? nk : 0) ||
+      overlap(d_logits, nz, loss_grad, loss_grad ? sz(E, 4) : 0) ||
+      overlap(d_logits, nz, d_loss, d_loss ? 4 : 0))
+    return FP8BL_ERR_OVERLAP;
+  const DeviceInfo* d = nullptr;
+  fp8bl_status st = current_device(&d);
+  if (st != FP8BL_OK) return st;
+  return from_cuda(launch_route_backward(logits, logits_type == FP8BL_F32, ids, d_weights,
+                                         loss_grad, d_loss, T, E, k, scoring == FP8BL_SIGMOID,
+                                         renormalize != 0, scale, d_logits, d->sm_count,
+                                         as_cuda(stream)));
+}
+
+static bool group_dims_ok(int64_t n, int64_t G) {
+  return dim_ok(n, true) && G >= 1 && G <= kMaxExperts;
+}
+
+size_t fp8bl_group_rows_workspace_bytes(int64_t n, int64_t G) {
+  return group_dims_ok(n, G) ? group_rows_workspace_bytes(n, G) : 0;
+}
+
+fp8bl_status fp8bl_group_rows(const int32_t* ids, int64_t n, int64_t G, int32_t* offsets,
+                              int32_t* order, int32_t* slot, void* workspace,
+                              size_t workspace_bytes, fp8bl_stream_t stream) {
+  if (!group_dims_ok(n, G)) return FP8BL_ERR_SHAPE;
+  if (!offsets || (n > 0 && (!ids || !order || !slot))) return FP8BL_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(slot, 4) ||
+      !aligned(workspace, 16))
+    return FP8BL_ERR_ALIGN;
+  const size_t nn = sz(n, 4), no = sz(G + 1, 4);
+  if (overlap(offsets, no, ids, nn) || overlap(order, nn, ids, nn) || overlap(slot, nn, ids, nn) ||
+      overlap(offsets, no, order, nn) || overlap(offsets, no, slot, nn) ||
+      overlap(order, nn, slot, nn))
+    return FP8BL_ERR_OVERLAP;
+  const DeviceInfo* d = nullptr;
+  fp8bl_status st = current_device(&d);
+  if (st != FP8BL_OK) return st;
+  const size_t need = group_rows_workspace_bytes(n, G);
+  if (need > 0) {
+    if (!workspace) return FP8BL_ERR_NULL;
+    if (workspace_bytes < need) return FP8BL_ERR_WORKSPACE;
+    if (overlap(workspace, need, ids, nn) || overlap(workspace, need, offsets, no) ||
+        overlap(workspace, need, order, nn) || overlap(workspace, need, slot, nn))
+      return FP8BL_ERR_OVERLAP;
+  }
+  return from_cuda(launch_group_rows(ids, n, G, offsets, order, slot, workspace, as_cuda(stream)));
+}
+
+static bool combine_dims_ok(int64_t T, int64_t n, int64_t k, int64_t H) {
+  return dim_ok(T, true) && dim_ok(n, true) && dim_ok(H, false) && H % 8 == 0 && k >= 1 &&
+         k <= kMaxTopK && T <= FP8BL_MAX_DIM / ((H + 1023) / 1024);
+}
+
+fp8bl_status fp8bl_combine_rows(const void* y_bf16, const float* weights, const int32_t* slot,
+                                const void* base_bf16, void* out_bf16, int64_t T, int64_t n,
+                                int64_t k, int64_t H, fp8bl_stream_t stream) {
+  if (!combine_dims_ok(T, n, k, H)) return FP8BL_ERR_SHAPE;
+  if (T == 0) return FP8BL_OK;
+  if ((n > 0 && !y_bf16) || !weights || !slot || !out_bf16) return FP8BL_ERR_NULL;
+  if (!aligned(y_bf16, 16) || !aligned(base_bf16, 16) || !aligned(out_bf16, 16) ||
+      !aligned(weights, 4) || !aligned(slot, 4))
+    return FP8BL_ERR_ALIGN;
+  const size_t no = sz(T, H) * 2, nk = sz(T, k) * 4;
+  if (overlap(out_bf16, no, y_bf16, sz(n, H) * 2) || overlap(out_bf16, no, weights, nk) ||
+      overlap(out_bf16, no, slot, nk) ||
+      (base_bf16 != out_bf16 && overlap(out_bf16, no, base_bf16, base_bf16 ? no : 0)))
+    return FP8BL_ERR_OVERLAP;
+  const DeviceInfo* d = nullptr;
+  fp8bl_status st = current_device(&d);
+  if (st != FP8BL_OK) return st;
+  return from_cuda(launch_combine_rows(y_bf16, weights, slot, base_bf16, out_bf16, T, n, k, H,
+                                       as_cuda(stream)));
+}
+
+fp8bl_status fp8bl_combine_rows_backward(const void* d_out_bf16, const void* y_bf16,
+                                         const float* weights, const int32_t* slot,
+                                         const int32_t* rows_used, void* d_y_bf16,
+                                         float* d_weights, int64_t T, int64_t n, int64_t k,
+                                         int64_t H, fp8bl_stream_t stream) {
+  if (!combine_dims_ok(T, n, k, H)) return FP8BL_ERR_SHAPE;
+  if (T == 0 && n == 0) return FP8BL_OK;
+  if ((n > 0 && (!y_bf16 || !d_y_bf16 || !rows_used)) ||
+      (T > 0 && (!d_out_bf16 || !weights || !slot || !d_weights)))
+    return FP8BL_ERR_NULL;
+  if (!aligned(d_out_bf16, 16) || !aligned(y_bf16, 16) || !aligned(d_y_bf16, 16) ||
+      !aligned(weights, 4) || !aligned(slot, 4) || !aligned(rows_used, 4) ||
+      !aligned(d_weights, 4))
+    return FP8BL_ERR_ALIGN;
+  const size_t ny = sz(n, H) * 2, no = sz(T, H) * 2, nk = sz(T, k) * 4;
+  if (overlap(d_y_bf16, ny, d_out_bf16, no) || overlap(d_y_bf16, ny, y_bf16, ny) ||
+      overlap(d_y_bf16, ny, weights, nk) || overlap(d_y_bf16, ny, slot, nk) ||
+      overlap(d_y_bf16, ny, rows_used, 4) || overlap(d_y_bf16, ny, d_weights, nk) ||
+      overlap(d_weights, nk, d_out_bf16, no) || overlap(d_weights, nk, y_bf16, ny) ||
+      overlap(d_weights, nk, weights, nk) || overlap(d_weights, nk, slot, nk) ||
+      overlap(d_weights, nk, rows_used, 4))
+    return FP8BL_ERR_OVERLAP;
+  const DeviceInfo* d = nullptr;
+  fp8bl_status st = current_device(&d);
+  if (st != FP8BL_OK) return st;
+  return from_cuda(launch_combine_rows_backward(d_out_bf16, y_bf16, weights, slot, rows_used,
+                                                d_y_bf16, d_weights, T, n, k, H, as_cuda(stream)));
+}
+
+static bool lora_dims_ok(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
+  return dim_ok(M, true) && dim_ok(N, false) && dim_ok(K, false) && N % 8 == 0 && K % 8 == 0 &&
+         R >= 8 && R <= kMaxRank && R % 8 == 0 && L >= 1 && L <= kMaxExperts;
+}
+
+size_t fp8bl_lora_add_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
+  if (!lora_dims_ok(M, N, K, R, L)) return 0;
+  const DeviceInfo* d = device_info();
+  return lora_workspace_bytes(M, N, K, R, L, d ? d->sm_count : 148);
+}
+
+fp8bl_status fp8bl_lora_add(const void* x_bf16, const void* a_bf16, const void* b_bf16,
+                            const float* scales, const int32_t* offsets, const int32_t* order,
+                            const void* y_bf16, void* out_bf16, int64_t M, int64_t N, int64_t K,
+                            int64_t R, int64_t L, void* workspace, size_t workspace_bytes,
+                            fp8bl_stream_t stream) {
+  if (!lora_dims_ok(M, N, K, R, L)) return FP8BL_ERR_SHAPE;
+  if (M == 0) return FP8BL_OK;
+  if (!x_bf16 || !a_bf16 || !b_bf16 || !offsets || !order || !y_bf16 || !out_bf16)
+    return FP8BL_ERR_NULL;
+  if (!aligned(x_bf16, 16) || !aligned(a_bf16, 16) || !aligned(b_bf16, 16) ||
+      !aligned(y_bf16, 16) || !aligned(out_bf16, 16) || !aligned(scales, 4) ||
+      !aligned(offsets, 4) || !aligned(order, 4) || !aligned(workspace, 16))
+    return FP8BL_ERR_ALIGN;
+  const size_t no = sz(M, N) * 2;
+  struct {
+    const void* p;
+    size_t n;
+  } in[] = {{x_bf16, sz(M, K) * 2},       {a_bf16, sz(L * R, K) * 2},
+            {b_bf16, sz(L * R, N) * 2},   {scales, scales ? sz(L, 4) : 0},
+            {offsets, sz(L + 1, 4)},      {order, sz(M, 4)},
+            {y_bf16, y_bf16 == out_bf16 ? 0 : no}};
+  for (const auto& b : in)
+    if (overlap(out_bf16, no, b.p, b.n)) return FP8BL_ERR_OVERLAP;
+  const DeviceInfo* d = nullptr;
+  fp8bl_status st = current_device(&d);
+  if (st != FP8BL_OK) return st;
+  const size_t need = lora_workspace_bytes(M, N, K, R, L, d->sm_count);
+  if (need > 0) {
+    if (!workspace) return FP8BL_ERR_NULL;
+    if (workspace_bytes < need) return FP8BL_ERR_WORKSPACE;
+    if (overlap(workspace, need, out_bf16, no)) return FP8BL_ERR_OVERLAP;
+    for (const auto& b : in)
+      if (overlap(workspace, need, b.p, b.n)) return FP8BL_ERR_OVERLAP;
+  }
+  return from_cuda(launch_lora_add(x_bf16, a_bf16, b_bf16, scales, offsets, order, y_bf16,
+                                   out_bf16, M, N, K, R, L, workspace, d->sm_count,
+                                   as_cuda(stream)));
 }
 
 namespace fp8bl {

@@ -106,6 +106,43 @@ cudaError_t launch_grouped_linear_ue8m0(const void* q_a, const uint8_t* s_a, con
                                         int64_t M, int64_t N, int64_t K, int64_t E,
                                         const DeviceInfo& dev, cudaStream_t st);
 
+// Router (route.cu): top-k of the logits [T, E], weights, counts, balance
+// loss and its slope; and the gradient with respect to the logits.
+constexpr int kMaxTopK = 32;
+size_t route_workspace_bytes(int64_t T, int64_t E, int sm_count);
+cudaError_t launch_route(const void* logits, bool f32, int64_t T, int64_t E, int64_t k,
+                         bool sigmoid, bool renorm, float scale, float balance,
+                         const uint8_t* mask, int32_t* ids, float* weights, int32_t* counts,
+                         float* loss, float* loss_grad, void* workspace, int sm_count,
+                         cudaStream_t st);
+cudaError_t launch_route_backward(const void* logits, bool f32, const int32_t* ids,
+                                  const float* d_weights, const float* loss_grad,
+                                  const float* d_loss, int64_t T, int64_t E, int64_t k,
+                                  bool sigmoid, bool renorm, float scale, void* d_logits,
+                                  int sm_count, cudaStream_t st);
+
+// Rows by group (rows.cu): stable sort of n group ids, and the weighted sum
+// of k rows per token with its gradient.
+size_t group_rows_workspace_bytes(int64_t n, int64_t G);
+cudaError_t launch_group_rows(const int32_t* ids, int64_t n, int64_t G, int32_t* offsets,
+                              int32_t* order, int32_t* slot, void* workspace, cudaStream_t st);
+cudaError_t launch_combine_rows(const void* y, const float* weights, const int32_t* slot,
+                                const void* base, void* out, int64_t T, int64_t n, int64_t k,
+                                int64_t H, cudaStream_t st);
+cudaError_t launch_combine_rows_backward(const void* d_out, const void* y, const float* weights,
+                                         const int32_t* slot, const int32_t* rows_used, void* d_y,
+                                         float* d_weights, int64_t T, int64_t n, int64_t k,
+                                         int64_t H, cudaStream_t st);
+
+// Low-rank adapters (lora.cu): out = y + s (x A^T) B^T for rows sorted by
+// adapter.
+constexpr int kMaxRank = 128;
+size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, int sm_count);
+cudaError_t launch_lora_add(const void* x, const void* a, const void* b, const float* scales,
+                            const int32_t* offsets, const int32_t* order, const void* y, void* out,
+                            int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, void* workspace,
+                            int sm_count, cudaStream_t st);
+
 // Largest M served by the decode (swap-AB, stream-K) schedule.
 constexpr int64_t kDecodeMaxM = 64;
 

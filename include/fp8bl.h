@@ -352,6 +352,164 @@ fp8bl_status fp8_linear_rowwise(const void *q_a, const float *s_a,
                                 void *y_bf16, int64_t M, int64_t N, int64_t K,
                                 fp8bl_stream_t stream);
 
+/*
+ * Rows of several experts or adapters.
+ *
+ * The calls around fp8_grouped_linear_ue8m0 and, for low-rank adapters,
+ * around any of the linears:
+ *   fp8bl_route          router logits -> the experts of each token, their
+ *                        weights, the tokens per expert and the balance loss
+ *   fp8bl_group_rows     ids -> rows sorted by expert or adapter
+ *   fp8bl_combine_rows   the experts' rows weighted and summed per token
+ *   fp8bl_lora_add       low-rank adapters of many requests on top of a
+ *                        linear's output
+ * and the gradients of the router and of the weighted sum (the experts'
+ * weights are frozen fp8 and have none).
+ */
+
+typedef enum { FP8BL_BF16 = 0, FP8BL_F32 = 1 } fp8bl_type;
+typedef enum { FP8BL_SOFTMAX = 0, FP8BL_SIGMOID = 1 } fp8bl_scoring;
+
+#define FP8BL_MAX_GROUPS 1024    /* experts, or adapters                   */
+#define FP8BL_MAX_TOP_K 32       /* experts per token                      */
+#define FP8BL_MAX_RANK 128       /* rank of an adapter                     */
+
+/*
+ * fp8bl_route -- for every row z of the logits:
+ *   softmax: score_e = share_e = exp(z_e) / sum exp(z);
+ *   sigmoid: score_e = 1 / (1 + exp(-z_e)), share_e = score_e / sum score;
+ *   the k experts of the largest logits, ties to the lowest index;
+ *   weight_j = scale * score_j, with `renormalize` scale * score_j / (sum of
+ *   the row's chosen scores);
+ * and over all rows, with c_e the times expert e was chosen and n the rows
+ * that chose any:
+ *   loss = balance * E / (k n^2) * sum_e c_e * sum_t share_te,
+ *   loss_grad_e = balance * E * c_e / (k n^2), the gradient with respect to
+ *   share_te (the same for every row; c_e counts as a constant).
+ * An expert whose logit is -inf or NaN is never chosen; slots left over have
+ * id -1 and weight 0, and a row that chooses nothing adds nothing to counts,
+ * n and loss.  A NaN logit next to chosen experts makes the row's share, and
+ * so the loss, NaN.  All arithmetic is fp32, the final sums of the loss fp64.
+ *
+ *   logits  in : [T, E], logits_type FP8BL_BF16 or FP8BL_F32
+ *   mask    in : one byte per row, 0 = the row (padding, whatever it holds)
+ *                chooses nothing; NULL = every row takes part
+ *   ids     out: int32 [T, k], in the order of falling logits
+ *   weights out: fp32 [T, k]          counts out: int32 [E]
+ *   loss    out: fp32 [1] or NULL     loss_grad out: fp32 [E] or NULL
+ *   workspace: at least fp8bl_route_workspace_bytes(T, E) bytes (16-byte
+ *              aligned), or NULL when that is 0; contents ignored.
+ *   T >= 0 (T == 0 writes counts, loss and loss_grad: zeros), 1 <= E <= 1024,
+ *   1 <= k <= min(E, 32), scale and balance finite.
+ */
+size_t fp8bl_route_workspace_bytes(int64_t T, int64_t E);
+fp8bl_status fp8bl_route(const void *logits, int logits_type, int64_t T, int64_t E, int64_t k,
+                         int scoring, int renormalize, float scale, float balance,
+                         const uint8_t *mask, int32_t *ids, float *weights, int32_t *counts,
+                         float *loss, float *loss_grad, void *workspace,
+                         size_t workspace_bytes, fp8bl_stream_t stream);
+
+/*
+ * fp8bl_route_backward -- the gradient of
+ *   sum_tj d_weights_tj weight_tj + d_loss * loss
+ * with respect to the logits, from fp8bl_route's inputs and outputs.
+ *
+ *   logits    in : as given to fp8bl_route     ids in: as it wrote them (an
+ *                  id outside [0, E) counts as -1)
+ *   d_weights in : fp32 [T, k] or NULL (no gradient through the weights)
+ *   loss_grad in : fp32 [E] from fp8bl_route, or NULL (none through the loss)
+ *   d_loss    in : fp32 [1] on the device, or NULL for 1
+ *   d_logits  out: [T, E] of the logits' type; zeros in rows that chose
+ *                  nothing
+ *   sizes and options as fp8bl_route; T == 0 enqueues nothing.
+ */
+fp8bl_status fp8bl_route_backward(const void *logits, int logits_type, const int32_t *ids,
+                                  const float *d_weights, const float *loss_grad,
+                                  const float *d_loss, int64_t T, int64_t E, int64_t k,
+                                  int scoring, int renormalize, float scale, void *d_logits,
+                                  fp8bl_stream_t stream);
+
+/*
+ * fp8bl_group_rows -- sorts n entries by their group, keeping the order of
+ * entries within a group.  Entries whose id is outside [0, G) have no group
+ * and come last.
+ *
+ *   ids     in : int32 [n] (for a router's [T, k] ids, entry t k + j)
+ *   offsets out: int32 [G + 1], group g owns sorted rows [offsets[g],
+ *                offsets[g + 1]); offsets[0] = 0, offsets[G] = entries with
+ *                a group.  What fp8_grouped_linear_ue8m0 and fp8bl_lora_add
+ *                take.
+ *   order   out: int32 [n], the entry in each sorted row
+ *   slot    out: int32 [n], the sorted row of each entry, -1 without a group
+ *   workspace: at least fp8bl_group_rows_workspace_bytes(n, G) bytes (16-byte
+ *              aligned), or NULL when that is 0; contents ignored.
+ *   n >= 0 (n == 0 writes offsets: zeros), 1 <= G <= 1024.
+ */
+size_t fp8bl_group_rows_workspace_bytes(int64_t n, int64_t G);
+fp8bl_status fp8bl_group_rows(const int32_t *ids, int64_t n, int64_t G, int32_t *offsets,
+                              int32_t *order, int32_t *slot, void *workspace,
+                              size_t workspace_bytes, fp8bl_stream_t stream);
+
+/*
+ * fp8bl_combine_rows -- out_t = base_t + sum_j weights_tj * y[slot_tj], added
+ * in fp32 in the order of j and rounded once to bf16.  Entries whose slot is
+ * outside [0, n) add nothing and their weight is not read.
+ *
+ *   y    in : bf16 [n, H]        weights in: fp32 [T, k]   slot in: int32 [T, k]
+ *   base in : bf16 [T, H] or NULL (zeros); may be `out` itself
+ *   out  out: bf16 [T, H]
+ *   T, n >= 0 (T == 0 enqueues nothing), H > 0, H % 8 == 0, 1 <= k <= 32,
+ *   T * ceil(H / 1024) <= FP8BL_MAX_DIM.
+ *
+ * fp8bl_combine_rows_backward -- from d_out, the gradient with respect to
+ * out: d_y[slot_tj] = weights_tj * d_out_t (rounded once to bf16) and
+ * d_weights_tj = <d_out_t, y[slot_tj]> (summed in fp32; 0 where the slot is
+ * outside [0, n)).  No two entries may have the same slot, as
+ * fp8bl_group_rows makes them.
+ *   rows_used in : int32 on the device, the number of rows that slots name
+ *                  (offsets[G] of fp8bl_group_rows): rows of d_y from there
+ *                  on are written as zeros
+ *   d_y out: bf16 [n, H]         d_weights out: fp32 [T, k]
+ */
+fp8bl_status fp8bl_combine_rows(const void *y_bf16, const float *weights, const int32_t *slot,
+                                const void *base_bf16, void *out_bf16, int64_t T, int64_t n,
+                                int64_t k, int64_t H, fp8bl_stream_t stream);
+fp8bl_status fp8bl_combine_rows_backward(const void *d_out_bf16, const void *y_bf16,
+                                         const float *weights, const int32_t *slot,
+                                         const int32_t *rows_used, void *d_y_bf16,
+                                         float *d_weights, int64_t T, int64_t n, int64_t k,
+                                         int64_t H, fp8bl_stream_t stream);
+
+/*
+ * fp8bl_lora_add -- low-rank adapters of many requests at once beside a
+ * shared projection: for the rows i of adapter l
+ *   out_i = y_i + scales_l * (x_i A_l^T) B_l^T,
+ * y being the projection's output (of any linear above).  The inner product
+ * is kept in fp32 (multiplied as two bf16 terms of 16 significant bits) and
+ * out is rounded once.  Rows without an adapter: out_i = y_i.
+ *
+ *   x bf16 in [M, K]     a bf16 in [L, R, K]     b bf16 in [L, N, R]
+ *   scales  in : fp32 [L] or NULL (ones)
+ *   offsets in : int32 [L + 1], order in: int32 [M], the rows sorted by
+ *            adapter as fp8bl_group_rows writes them (every row named once;
+ *            rows behind offsets[L] have no adapter).  Made once for a batch,
+ *            they serve every projection of every layer.  Values are clamped
+ *            or skipped by the kernels, so malformed ones cannot make them
+ *            read or write out of bounds.
+ *   y       in : bf16 [M, N]      out out: bf16 [M, N], may be y itself
+ *   workspace: at least fp8bl_lora_add_workspace_bytes(M, N, K, R, L) bytes
+ *            (16-byte aligned), or NULL when that is 0; contents ignored.
+ *   M >= 0 (M == 0 enqueues nothing), N, K > 0 and multiples of 8, R a
+ *   multiple of 8 up to 128 (pad adapters of smaller rank with zeros),
+ *   1 <= L <= 1024.
+ */
+size_t fp8bl_lora_add_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L);
+fp8bl_status fp8bl_lora_add(const void *x_bf16, const void *a_bf16, const void *b_bf16,
+                            const float *scales, const int32_t *offsets, const int32_t *order,
+                            const void *y_bf16, void *out_bf16, int64_t M, int64_t N, int64_t K,
+                            int64_t R, int64_t L, void *workspace, size_t workspace_bytes,
+                            fp8bl_stream_t stream);
+
 /* Workspace sizes (bytes) the two linear calls need for these sizes on the
  * current device; 0 when no scratch is needed.  Never fails: invalid sizes
  * return 0 (the linear call then reports the error). */
