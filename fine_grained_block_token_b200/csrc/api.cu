@@ -608,7 +608,8 @@ fp8bl_status fp8bl_combine_rows_backward(const void* d_out_bf16, const void* y_b
 
 static bool lora_dims_ok(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
   return dim_ok(M, true) && dim_ok(N, false) && dim_ok(K, false) && N % 8 == 0 && K % 8 == 0 &&
-         R >= 8 && R <= kMaxRank && R % 8 == 0 && L >= 1 && L <= kMaxExperts;
+         R >= 8 && R <= kMaxRank && R % 8 == 0 && L >= 1 && L <= kMaxExperts &&
+         L * N <= FP8BL_MAX_DIM;
 }
 
 size_t fp8bl_lora_add_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
@@ -652,8 +653,7 @@ fp8bl_status fp8bl_lora_add(const void* x_bf16, const void* a_bf16, const void* 
       if (overlap(workspace, need, b.p, b.n)) return FP8BL_ERR_OVERLAP;
   }
   return from_cuda(launch_lora_add(x_bf16, a_bf16, b_bf16, scales, offsets, order, y_bf16,
-                                   out_bf16, M, N, K, R, L, workspace, d->sm_count,
-                                   as_cuda(stream)));
+                                   out_bf16, M, N, K, R, L, workspace, *d, as_cuda(stream)));
 }
 
 namespace fp8bl {

@@ -141,7 +141,7 @@ size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t 
 cudaError_t launch_lora_add(const void* x, const void* a, const void* b, const float* scales,
                             const int32_t* offsets, const int32_t* order, const void* y, void* out,
                             int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, void* workspace,
-                            int sm_count, cudaStream_t st);
+                            const DeviceInfo& dev, cudaStream_t st);
 
 // Largest M served by the decode (swap-AB, stream-K) schedule.
 constexpr int64_t kDecodeMaxM = 64;
