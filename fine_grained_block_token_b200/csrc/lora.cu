@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const Args p) {
           *reinterpret_cast<float2*>(&mine[(h * 8 + g) * RP + n * 8 + q * 2]) =
               make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
     __syncthreads();
-    float* up = p.u + (static_cast<int64_t>(c) * p.M + tile.pos) * RP;
+    float* up = reinterpret_cast<float*>(p.u) + (static_cast<int64_t>(c) * p.M + tile.pos) * RP;
     for (int i = threadIdx.x * 4; i < tile.rows * RP; i += kThreads * 4) {
       float4 v = *reinterpret_cast<const float4*>(part + i);
 #pragma unroll
@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const Args p) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = h * 8 + g;
-      const float* up = p.u + static_cast<int64_t>(tile.pos + (r < tile.rows ? r : 0)) * RP;
+      const float* up = reinterpret_cast<const float*>(p.u) +
+                        static_cast<int64_t>(tile.pos + (r < tile.rows ? r : 0)) * RP;
       const int64_t stride = static_cast<int64_t>(p.M) * RP;
       constexpr int kRun = kRT == 1 ? 4 : 8;  // neighbouring ranks of a lane
 #pragma unroll
@@ -321,6 +322,7 @@ Plan plan_lora(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, int sm_cou
   const int64_t sr = sm_count * (p.rt <= 4 ? 2 : 1), er = sm_count * (p.rt <= 2 ? 2 : 1);
   p.shrink_blocks = static_cast<int>(sb < sr ? sb : sr);
   p.expand_blocks = static_cast<int>(eb < er ? eb : er);
+  p.u_bytes = static_cast<size_t>(p.max_splits) * static_cast<size_t>(M) * 16 * p.rt * 4;
   return p;
 }
 
@@ -358,8 +360,7 @@ cudaError_t launch_rank(const Args& a, const Plan& pl, cudaStream_t st) {
 
 size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, int sm_count) {
   if (M == 0) return 0;
-  const Plan p = plan_lora(M, N, K, R, L, sm_count);
-  return static_cast<size_t>(p.max_splits) * static_cast<size_t>(M) * 16 * p.rt * 4;
+  return plan_lora(M, N, K, R, L, sm_count).u_bytes;
 }
 
 cudaError_t launch_lora_add(const void* x, const void* a, const void* b, const float* scales,
@@ -376,7 +377,7 @@ cudaError_t launch_lora_add(const void* x, const void* a, const void* b, const f
   r.order = order;
   r.y = static_cast<const __nv_bfloat16*>(y);
   r.out = static_cast<__nv_bfloat16*>(out);
-  r.u = static_cast<float*>(workspace);
+  r.u = static_cast<__nv_bfloat16*>(workspace);
   r.M = static_cast<int>(M);
   r.N = static_cast<int>(N);
   r.K = static_cast<int>(K);

@@ -21,10 +21,12 @@ struct Args {
   const int32_t* order;
   const __nv_bfloat16* y;
   __nv_bfloat16* out;
-  float* u;             // [parts of K][M][RP], sorted rows, rank padded to RP
+  // u of the sorted rows, rank padded to RP.  Small batches: fp32 [parts of K]
+  // [M][RP]; long ones: bf16 [M][hi RP | lo RP], scaled.
+  __nv_bfloat16* u;
   int M, N, K, R, L;
-  int max_splits;       // parts of K that the workspace holds
-  int shrink_blocks;    // blocks of the shrink kernel: its parts follow from it
+  int max_splits;       // parts of K at most (long batches: exactly)
+  int shrink_blocks;    // blocks of the shrink kernel
   int copy_rest;        // rows without an adapter are copied from y to out
   int* err;
 };
@@ -34,6 +36,7 @@ struct Plan {
   int rt;
   int shrink_blocks, expand_blocks;
   int max_splits;
+  size_t u_bytes;
 };
 inline int rank_tiles(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 

@@ -5,12 +5,16 @@
 // Shrink, u = x A^T: bound by reading x.  128 threads copy 64-deep slices of
 // the tile's rows (wherever `order` says they are) and of A into a ring of
 // 128-byte-swizzled shared-memory stages with cp.async; one thread issues the
-// MMAs.  K is split so that all blocks have work; every part writes its own
-// fp32 u and the expand adds the parts in order.
+// MMAs.  K is split over the blocks of a cluster so that all SMs have work;
+// the blocks' sums meet through distributed shared memory, added in the order
+// of the parts, and leave as two bf16 terms side by side ([hi | lo], 2 RP
+// deep).  (Parts that the expand adds up instead cost 38 of 137 us beside
+// 28672 x 4096 at rank 64 and 4096 rows: every block of the expand read all
+// seven.)
 //
-// Expand, out = y + s u B^T: bound by reading y and writing out.  u becomes
-// two bf16 terms side by side ([hi | lo], 2 RP deep), so that one accumulation
-// over both with B read twice gives the product of the 16-bit u.  Work is
+// Expand, out = y + s u B^T: bound by reading y and writing out.  One
+// accumulation over hi and lo with B read twice multiplies by all 16 bits of
+// u.  Work is
 // numbered in chunks of 64 columns, tile after tile, and every block takes an
 // equal run of chunks.  Of a chunk, B comes by TMA, the MMAs run into one of
 // two halves of tensor memory, and the 128 epilogue threads stream y through
@@ -51,11 +55,14 @@ template <int kRT>
 struct ShrinkShape {
   static constexpr int RP = 16 * kRT;
   static constexpr int kTmem = RP < 32 ? 32 : RP;  // columns, at least 32
+  static constexpr int kQuads = RP / 4;            // 16-byte quads of a row of sums
+  static constexpr int kSwizzle = kQuads < 8 ? kQuads - 1 : 7;
   static constexpr int kStages = kRT <= 2 ? 5 : kRT == 4 ? 4 : 3;
   static constexpr int kA = RP * 128;  // bytes of A per stage
   static constexpr int kStage = kBlock + kA;
   static constexpr int kAhead = kStages == 3 ? 2 : kStages - 2;  // stages on their way
   static constexpr int kSmem = kStages * kStage + 1024;
+  static_assert(kRows * RP * 4 <= kStages * kStage, "the sums fit the ring");
 };
 
 constexpr int kShrinkThreads = 160;  // 4 copying warps, 1 MMA warp
@@ -92,15 +99,16 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tiles_kernel(co
   ptx::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_holder);
   const int tiles = map.before[p.L];
-  const int parts = lora::parts_of_k(p.shrink_blocks, tiles, p.max_splits);
+  const int parts = p.max_splits;  // blocks of a cluster, one part of K each
+  const int part = static_cast<int>(ptx::cluster_ctarank());
+  const int clusters = gridDim.x / parts;
   const int blocks_k = (p.K + kDeep - 1) / kDeep;
   bool ok = true;
   uint32_t n_used = 0;  // stages used so far
   uint32_t item_phase = 0;
 
-  for (int item = blockIdx.x; item < tiles * parts; item += gridDim.x, item_phase ^= 1) {
-    const Tile tile = map.find(item / parts, p.L, kRows);
-    const int part = item % parts;
+  for (int t = blockIdx.x / parts; t < tiles; t += clusters, item_phase ^= 1) {
+    const Tile tile = map.find(t, p.L, kRows);
     const int k0 = static_cast<int>(static_cast<int64_t>(blocks_k) * part / parts);
     const int n = static_cast<int>(static_cast<int64_t>(blocks_k) * (part + 1) / parts) - k0;
     if (warp < 4) {
@@ -152,30 +160,27 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tiles_kernel(co
         ok = false;
       }
       ptx::tc_fence_after();
+      // this part's sums, a row per thread, into the ring (the MMAs are
+      // through with it); 16-byte quads swizzled by row against bank conflicts
       const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-      const bool row_in = static_cast<int>(threadIdx.x) < tile.rows;
-      float* up = p.u + (static_cast<int64_t>(part) * p.M + tile.pos +
-                         (row_in ? static_cast<int>(threadIdx.x) : 0)) * S::RP;
+      uint4* row = reinterpret_cast<uint4*>(smem) + threadIdx.x * S::kQuads;
+      const int sw = threadIdx.x & S::kSwizzle;
       if constexpr (kRT == 1) {
         uint32_t v[16];
         ptx::tmem_ld_32x32b_x16(lane_base, v);
         ptx::tmem_ld_wait();
-        if (row_in)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            reinterpret_cast<uint4*>(up)[j] =
-                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        for (int j = 0; j < 4; ++j)
+          row[j ^ sw] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
       } else {
 #pragma unroll
         for (int h = 0; h < kRT / 2; ++h) {
           uint32_t v[32];
           ptx::tmem_ld_32x32b_x32(lane_base + 32 * h, v);
           ptx::tmem_ld_wait();
-          if (row_in)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              reinterpret_cast<uint4*>(up)[8 * h + j] =
-                  make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          for (int j = 0; j < 8; ++j)
+            row[(8 * h + j) ^ sw] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
       }
       // the next item's MMAs start behind these reads: they wait for stages
@@ -205,6 +210,36 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tiles_kernel(co
       }
     }
     n_used += n;
+    __syncwarp();
+    ptx::cluster_sync();
+    // every block adds up its share of the rows over all parts, in order
+    if (warp < 4) {
+      const int share = kRows / parts, r_first = part * share;
+      const float scale = p.scales ? p.scales[tile.group] : 1.0f;
+      __nv_bfloat16* up = p.u + static_cast<int64_t>(tile.pos) * (2 * S::RP);
+      for (int f = threadIdx.x; f < share * S::kQuads; f += 128) {
+        const int r = r_first + f / S::kQuads, j = f % S::kQuads;
+        if (r >= tile.rows) break;
+        const uint32_t at = base + (r * S::kQuads + (j ^ (r & S::kSwizzle))) * 16;
+        float4 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < parts) v[c] = ptx::ld_cluster_f4(ptx::map_to_cta(at, c));
+#pragma unroll
+        for (int c = 1; c < 8; ++c)
+          if (c < parts) v[0].x += v[c].x, v[0].y += v[c].y, v[0].z += v[c].z, v[0].w += v[c].w;
+        uint2 hi, lo;
+        // ranks past R are padding (their sum is NaN beside an infinite x)
+        if (4 * j >= p.R) v[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        lora::split2(v[0].x * scale, v[0].y * scale, hi.x, lo.x);
+        lora::split2(v[0].z * scale, v[0].w * scale, hi.y, lo.y);
+        __nv_bfloat16* o = up + static_cast<int64_t>(r) * (2 * S::RP) + 4 * j;
+        *reinterpret_cast<uint2*>(o) = hi;
+        *reinterpret_cast<uint2*>(o + S::RP) = lo;
+      }
+    }
+    __syncwarp();
+    ptx::cluster_sync();  // the ring is free again, here and for the others' reads
   }
   ptx::cp_async_wait<0>();
   ptx::tc_fence_before();
@@ -277,7 +312,6 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
   ptx::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_holder);
   const int groups = p.L + p.copy_rest;
-  const int parts = lora::parts_of_k(p.shrink_blocks, map.before[p.L], p.max_splits);
   const int chunks = (p.N + kCols - 1) / kCols;
   const int64_t total = static_cast<int64_t>(map.before[groups]) * chunks;
   int64_t at = total * blockIdx.x / gridDim.x;
@@ -325,34 +359,19 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
         waited = true;
       }
       if (!rest) {
-        // u of this thread's row, its parts of K in order, as [hi | lo].  The
-        // MMAs that read the last tile's u are done: their results were read.
-        const int r = threadIdx.x;
-        const float scale = p.scales ? p.scales[tile.group] : 1.0f;
-        const float* up = p.u + static_cast<int64_t>(tile.pos + (r < tile.rows ? r : 0)) * S::RP;
-        const int64_t stride = static_cast<int64_t>(p.M) * S::RP;
-#pragma unroll
-        for (int i = 0; i < S::RP / 8; ++i) {
-          float v[8] = {};
-          // ranks past R are padding (their u is NaN beside an infinite x)
-          if (r < tile.rows && i * 8 < p.R) {
-#pragma unroll 4
-            for (int c = 0; c < parts; ++c) {
-              const float4 a = *reinterpret_cast<const float4*>(up + c * stride + i * 8);
-              const float4 b = *reinterpret_cast<const float4*>(up + c * stride + i * 8 + 4);
-              v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-              v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-            }
-          }
-          uint4 hi, lo;
-          lora::split2(v[0] * scale, v[1] * scale, hi.x, lo.x);
-          lora::split2(v[2] * scale, v[3] * scale, hi.y, lo.y);
-          lora::split2(v[4] * scale, v[5] * scale, hi.z, lo.z);
-          lora::split2(v[6] * scale, v[7] * scale, hi.w, lo.w);
-          const int ch = i, cl = S::RP / 8 + i;  // 16-byte chunks of the 2 RP deep row
-          *reinterpret_cast<uint4*>(u_s + (ch / 8) * kBlock + cell(r, ch % 8)) = hi;
-          *reinterpret_cast<uint4*>(u_s + (cl / 8) * kBlock + cell(r, cl % 8)) = lo;
+        // u of the tile, [hi | lo] as the shrink left it.  The MMAs that read
+        // the last tile's u are done: their results were read.
+        constexpr int kChunks = S::RP / 4;  // 16-byte chunks of a row
+        const __nv_bfloat16* up = p.u + static_cast<int64_t>(tile.pos) * (2 * S::RP);
+#pragma unroll 8
+        for (int i = 0; i < kChunks; ++i) {
+          const int f = i * 128 + threadIdx.x, r = f / kChunks, c = f % kChunks;
+          const bool in = r < tile.rows;
+          ptx::cp_async16(ptx::smem_u32(u_s) + (c / 8) * kBlock + cell(r, c % 8),
+                          up + (in ? f * 8 : 0), in);
         }
+        ptx::cp_async_commit();
+        ptx::cp_async_wait<0>();
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(u_full);
       }
@@ -377,10 +396,13 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
           ptx::mbar_arrive(t_empty(h));
           ptx::named_barrier_sync(1, 128);  // everyone's y has landed
           const int r = threadIdx.x;
+          uint4 v8[8];  // all reads before the writes that might alias them
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v8[c] = *reinterpret_cast<const uint4*>(slot + cell(r, c));
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint4* q = reinterpret_cast<uint4*>(slot + cell(r, c));
-            const uint4 v = *q;
+            const uint4 v = v8[c];
             auto f = [&](int k) {
               const int e = c * 8 + k;
               return __uint_as_float(e < 32 ? a0[e & 31] : a1[e & 31]);
@@ -393,20 +415,22 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
         // the cells this thread copied in are the ones it copies out, so the
         // next copy into the slot needs no barrier
         if (col0 + i * kCols < p.N) {
+          uint4 o[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (live >> j & 1)
-              *reinterpret_cast<uint4*>(p.out + off[j] + i * kCols) =
-                  *reinterpret_cast<const uint4*>(slot + mine + j * 2048);
+            o[j] = *reinterpret_cast<const uint4*>(slot + mine + j * 2048);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (live >> j & 1) *reinterpret_cast<uint4*>(p.out + off[j] + i * kCols) = o[j];
         }
       }
     } else if (warp == 4 && !rest) {
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_spin(u_full, u_phase));
+      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(u_full, u_phase));
       for (int i = 0; i < n && ok; ++i) {
         const uint32_t u = n_used + i, h = u & 1u;
         const int s = u % S::kBStages;
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait_spin(b_full(s), (u / S::kBStages) & 1u) &&
-                                         ptx::mbar_wait_spin(t_empty(h), ((u >> 1) & 1u) ^ 1u));
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(b_full(s), (u / S::kBStages) & 1u) &&
+                                         ptx::mbar_wait(t_empty(h), ((u >> 1) & 1u) ^ 1u));
         if (!ok) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
@@ -465,17 +489,20 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
 // ------------------------------------------------------------------- host
 
 template <typename Kernel, typename... Ts>
-cudaError_t launch_pdl(Kernel k, int blocks, int threads, size_t smem, cudaStream_t st,
-                       const Ts&... args) {
+cudaError_t launch_pdl(Kernel k, int blocks, int threads, size_t smem, int cluster,
+                       cudaStream_t st, const Ts&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   set_programmatic_serialization(at[0]);
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
@@ -498,10 +525,10 @@ cudaError_t launch_rank(const Args& a, const lora::Plan& pl, cudaStream_t st) {
                     kCols, 128))
     return cudaErrorInvalidValue;
   e = launch_pdl(lora_shrink_tiles_kernel<kRT>, pl.shrink_blocks, kShrinkThreads,
-                 ShrinkShape<kRT>::kSmem, st, a);
+                 ShrinkShape<kRT>::kSmem, pl.max_splits, st, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(lora_expand_tiles_kernel<kRT>, pl.expand_blocks, kExpandThreads,
-                    ExpandShape<kRT>::kSmem, st, tb, a);
+                    ExpandShape<kRT>::kSmem, 1, st, tb, a);
 }
 
 }  // namespace
@@ -511,14 +538,20 @@ namespace lora {
 Plan plan_tiles(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, int sm_count) {
   Plan p;
   p.rt = rank_tiles(R);
-  const int64_t tiles = M / kRows + (L + 1 < M ? L + 1 : M);
-  // a part of K is at least 256 deep
-  const int64_t parts = (K + 255) / 256;
-  p.max_splits = static_cast<int>(parts < 16 ? parts : 16);
-  const int64_t sb = tiles * p.max_splits, eb = tiles * ((N + kCols - 1) / kCols);
-  const int64_t sr = sm_count * 2, er = sm_count * (p.rt == 8 ? 1 : 2);
-  p.shrink_blocks = static_cast<int>(sb < sr ? sb : sr);
+  const int64_t least = (M + kRows - 1) / kRows, most = M / kRows + (L + 1 < M ? L + 1 : M);
+  // Blocks of a cluster: as many as keep the tiles that are likely (full ones
+  // and a partial one for each adapter) resident at once, two blocks per SM,
+  // with at least 256 of K each.
+  const int64_t likely = least + (L < least ? L : least);
+  p.max_splits = 1;
+  while (p.max_splits < 8 && likely * p.max_splits * 2 <= 2 * sm_count &&
+         K >= 512 * static_cast<int64_t>(p.max_splits))
+    p.max_splits *= 2;
+  const int64_t clusters = 2 * sm_count / p.max_splits;
+  p.shrink_blocks = static_cast<int>((most < clusters ? most : clusters) * p.max_splits);
+  const int64_t eb = most * ((N + kCols - 1) / kCols), er = sm_count * (p.rt == 8 ? 1 : 2);
   p.expand_blocks = static_cast<int>(eb < er ? eb : er);
+  p.u_bytes = static_cast<size_t>(M) * 16 * p.rt * 4;  // [hi | lo] in bf16
   return p;
 }
 

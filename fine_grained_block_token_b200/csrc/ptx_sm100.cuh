@@ -394,6 +394,16 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+// 16 bytes from any CTA's shared memory (a shared::cluster address).
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // Bulk copy of `bytes` (a multiple of 16) from this CTA's shared memory to
 // `dst` in any CTA of the cluster; completion is counted in bytes on the
 // mbarrier `bar` of the destination CTA (both shared::cluster addresses).
