@@ -10,9 +10,9 @@
 //   w_j = scale * score_j, or scale * score_j / sum of the chosen scores
 //   loss = balance * E / (k n^2) * sum_e c_e sum_t share_te over the n rows
 //   that chose anything; slope_e = balance * E * c_e / (k n^2) = dloss/dshare.
-// Sigmoid shares and renormalised weights are formed from scores multiplied
-// by exp(-m), m = min(max z, 0): their ratios stay finite where every score
-// of a row underflows.
+// Where every logit of a row is far below zero, sigmoid shares and renormalised
+// weights are formed from scores multiplied by exp(-max z): their ratios stay
+// finite where the scores themselves underflow.
 //
 // A row belongs to kLanes lanes of a warp and a lane holds kVals neighbouring
 // logits, so one pass over the logits serves the choice, the scores and the
@@ -30,7 +30,11 @@
 namespace fp8bl {
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a block: as many as the registers of an SM allow, since a row is
+// a long chain of short steps and only other rows can fill the gaps.
+template <int kVals>
+constexpr int kForward = kVals <= 8 ? 1024 : kVals == 16 ? 512 : 256;
+constexpr int kThreads = 256;  // of the gradient
 constexpr unsigned kFull = 0xffffffffu;
 
 // Logit as a 32-bit key that orders like the float; 0 = never chosen (-inf,
@@ -59,17 +63,6 @@ __device__ __forceinline__ uint32_t max_lanes(uint32_t v) {
   } else {
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
-    return v;
-  }
-}
-
-template <int kLanes>
-__device__ __forceinline__ uint32_t min_lanes(uint32_t v) {
-  if constexpr (kLanes == 32) {
-    return __reduce_min_sync(kFull, v);
-  } else {
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(kFull, v, o));
     return v;
   }
 }
@@ -137,29 +130,45 @@ __device__ __forceinline__ void store_vals(T* p, int valid, bool vec, const floa
   }
 }
 
-// Scores of a row from its logits.  e[i] is the score times a factor common
-// to the row (softmax: 1 / p's denominator; sigmoid: exp(-m)), inv_sum the
-// reciprocal of their sum over the row, so e * inv_sum is the share.
+// Sigmoid of z and of -z with one exponential: t = exp(-|z|) <= 1, so neither
+// overflows and 1 - s keeps its digits.
+__device__ __forceinline__ void sigmoid2(float z, float& s, float& not_s) {
+  const float t = __expf(-fabsf(z));
+  const float r = __fdividef(1.0f, 1.0f + t);
+  s = z < 0.0f ? t * r : r;
+  not_s = z < 0.0f ? r : t * r;
+}
+
+// Scores of a row from its logits: e[i] is the score times a factor common to
+// the row (softmax: its denominator; sigmoid: 1, or exp(-m) where every logit
+// is below kFar and scores might underflow), so e / sum is the share.  The
+// many use the fast exponential (off by 2^-22 |z - m| at most); value() of the
+// chosen few the accurate one.
+constexpr float kFar = -60.0f;
+
 template <int kLanes, int kVals, bool kSigmoid>
 struct RowScores {
   float shift, sum;
+  bool far;
 
   __device__ __forceinline__ float value(float z) const {
-    if constexpr (kSigmoid) {
-      // exp(-m) / (1 + exp(-z)) = exp(z - m) / (1 + exp(z)) where m < 0
-      return shift < 0.0f ? expf(z - shift) / (1.0f + expf(z)) : 1.0f / (1.0f + expf(-z));
-    } else {
-      return expf(z - shift);
-    }
+    if (kSigmoid && !far) return 1.0f / (1.0f + expf(-z));
+    return expf(z - shift);  // below kFar, 1 + exp(z) is 1
   }
 
   __device__ __forceinline__ RowScores(uint32_t top, const float (&z)[kVals], float (&e)[kVals]) {
-    const float m = key_logit(top);
-    shift = kSigmoid ? fminf(m, 0.0f) : m;
+    shift = key_logit(top);
+    far = kSigmoid && shift < kFar;
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
-      e[i] = value(z[i]);
+      float unused;
+      if constexpr (kSigmoid) {
+        sigmoid2(z[i], e[i], unused);
+        if (far) e[i] = __expf(z[i] - shift);
+      } else {
+        e[i] = __expf(z[i] - shift);
+      }
       s += e[i];
     }
     sum = sum_lanes<kLanes>(s);
@@ -188,25 +197,66 @@ __device__ __forceinline__ double loss_slope(float balance, int E, int k, int ro
   return static_cast<double>(balance) * E / (static_cast<double>(k) * n * n);
 }
 
+// A lane's largest key and, as long as `both`, its second largest, with their
+// places (the lower place of two equal keys first).  A lane seldom wins more
+// than one of the k rounds, so the second is at hand when it does, and a scan
+// for more is rare.
+template <int kVals>
+struct Best {
+  uint32_t key, key2;
+  int at, at2;
+  bool both;
+
+  // The keys that come after (m, from) in the order of choice.
+  __device__ __forceinline__ void scan(const uint32_t (&k)[kVals], uint32_t m, int from) {
+    key = key2 = 0;
+    at = at2 = 0;
+    both = true;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) {
+      const uint32_t v = k[i] < m || (k[i] == m && i > from) ? k[i] : 0u;
+      if (v > key) {
+        key2 = key, at2 = at;
+        key = v, at = i;
+      } else if (v > key2) {
+        key2 = v, at2 = i;
+      }
+    }
+  }
+
+  __device__ __forceinline__ void pop(const uint32_t (&k)[kVals]) {
+    if (both) {
+      key = key2, at = at2;
+      both = false;
+    } else {
+      scan(k, key, at);
+    }
+  }
+};
+
 template <typename T, int kLanes, int kVals, bool kSigmoid>
-__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
-  constexpr int kRows = kThreads / kLanes;  // rows in flight per block
+__global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteArgs a) {
+  constexpr int kBlock = kForward<kVals>, kWarps = kBlock / 32;
+  constexpr int kRows = kBlock / kLanes;  // rows in flight per block
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  // [kRows][32] chosen ids and logits, then [E] counts, then sums [kRows][E]
+  // [kRows][32] chosen ids and logits, [E] counts, sums [kWarps][E]
   int* ch_id = reinterpret_cast<int*>(smem_raw);
   float* ch_z = reinterpret_cast<float*>(ch_id + kRows * 32);
   int* counts = reinterpret_cast<int*>(ch_z + kRows * 32);
   float* sums = reinterpret_cast<float*>(counts + a.E);
   __shared__ int rows_used;
-  __shared__ double red[kThreads / 32];
+  __shared__ double red[kWarps];
 
-  for (int e = threadIdx.x; e < a.E; e += kThreads) counts[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += kBlock) counts[e] = 0;
   if (threadIdx.x == 0) rows_used = 0;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   __syncthreads();
 
   const int g = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+  const int lane = threadIdx.x % 32;
+  // the lanes of this row group, as bits of the warp
+  const unsigned group = kLanes == 32 ? kFull : ((1u << (kLanes % 32)) - 1u) << (lane - l);
   const int first = l * kVals, valid = a.E - first;
   int* my_id = ch_id + g * 32;
   float* my_z = ch_z + g * 32;
@@ -233,32 +283,22 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < kVals; ++i) key[i] = choice_key(z[i]);
 
-    // k rounds of: largest key left among the lanes, lowest index among
-    // equals; the lane that held it looks up its next.
-    uint32_t best = 0, at = 0;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i)
-      if (key[i] > best) best = key[i], at = i;
+    // k rounds of: the largest key left, in the lowest lane that holds it
+    // (lanes hold rising indices, so that is the lowest index)
+    Best<kVals> best;
+    best.scan(key, 0xffffffffu, -1);
     uint32_t top = 0;
     for (int j = 0; j < a.k; ++j) {
-      const uint32_t m = max_lanes<kLanes>(best);
-      const uint32_t id = min_lanes<kLanes>(best == m ? first + at : 0xffffffffu);
+      const uint32_t m = max_lanes<kLanes>(best.key);
       if (j == 0) top = m;
-      if (l == 0) {
-        my_id[j] = m ? static_cast<int>(id) : -1;
+      const unsigned holders = __ballot_sync(kFull, best.key == m) & group;
+      if (lane == __ffs(holders) - 1) {
+        my_id[j] = m ? first + best.at : -1;
         my_z[j] = key_logit(m);
+        if (m) best.pop(key);
       }
-      if (m != 0 && id == first + at) {
-        uint32_t nb = 0, na = 0;
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) {
-          const bool left = key[i] < m || (key[i] == m && i > static_cast<int>(at));
-          if (left && key[i] > nb) nb = key[i], na = i;
-        }
-        best = nb, at = na;
-      }
+      __syncwarp();
     }
-    __syncwarp();
 
     float e[kVals];
     const RowScores<kLanes, kVals, kSigmoid> sc(top, z, e);
@@ -272,9 +312,11 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
     }
     // weights of the chosen
     float part = 0.0f;
-    for (int j = l; j < a.k; j += kLanes)
-      if (my_id[j] >= 0) part += sc.value(my_z[j]);
-    part = sum_lanes<kLanes>(part);
+    if (a.renorm) {
+      for (int j = l; j < a.k; j += kLanes)
+        if (my_id[j] >= 0) part += sc.value(my_z[j]);
+      part = sum_lanes<kLanes>(part);
+    }
     if (row < a.T) {
       for (int j = l; j < a.k; j += kLanes) {
         const int id = my_id[j];
@@ -299,21 +341,25 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
     __syncwarp();
   }
 
-  // block sums: each row group's registers, then over the groups in order
-  if (a.loss || a.loss_grad) {
+  // block sums: the row groups of a warp, then the warps in order
+  const bool want_share = a.loss != nullptr;
+  if (want_share) {
 #pragma unroll
-    for (int i = 0; i < kVals; ++i)
-      if (i < valid) sums[g * a.E + first + i] = acc[i];
+    for (int i = 0; i < kVals; ++i) {
+#pragma unroll
+      for (int o = kLanes; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(kFull, acc[i], o);
+      if (lane < kLanes && i < valid) sums[threadIdx.x / 32 * a.E + first + i] = acc[i];
+    }
   }
   if (my_rows) atomicAdd(&rows_used, my_rows);
   __syncthreads();
   const bool alone = gridDim.x == 1;
   const double slope = loss_slope(a.balance, a.E, a.k, rows_used);
   double term = 0.0;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+  for (int e = threadIdx.x; e < a.E; e += kBlock) {
     float s = 0.0f;
-    if (a.loss || a.loss_grad)
-      for (int r = 0; r < kRows; ++r) s += sums[r * a.E + e];
+    if (want_share)
+      for (int w = 0; w < kWarps; ++w) s += sums[w * a.E + e];
     if (alone) {
       a.counts[e] = counts[e];
       if (a.loss_grad) a.loss_grad[e] = static_cast<float>(slope * counts[e]);
@@ -327,14 +373,14 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
     if (threadIdx.x == 0) a.part_rows[blockIdx.x] = rows_used;
     return;
   }
-  if (!a.loss) return;
+  if (!want_share) return;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(kFull, term, o);
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = term;
+  if (lane == 0) red[threadIdx.x / 32] = term;
   __syncthreads();
   if (threadIdx.x == 0) {
     double t = 0.0;
-    for (int w = 0; w < kThreads / 32; ++w) t += red[w];
+    for (int w = 0; w < kWarps; ++w) t += red[w];
     *a.loss = static_cast<float>(t);
   }
 }
@@ -491,7 +537,11 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
 #pragma unroll
       for (int i = 0; i < kVals; ++i) {
         float v = e[i] * (up[i] - all);
-        if (kSigmoid) v *= 1.0f / (1.0f + expf(z[i]));  // 1 - s
+        if constexpr (kSigmoid) {
+          float s, not_s;
+          sigmoid2(z[i], s, not_s);
+          v *= not_s;
+        }
         d[i] = used ? v : 0.0f;
       }
       store_vals<T, kVals>(dr + first, valid, a.vec, d);
@@ -539,13 +589,13 @@ cudaError_t by_type(bool f32, bool sigmoid, int64_t E, F f) {
   return sigmoid ? by_width<__nv_bfloat16, true>(E, f) : by_width<__nv_bfloat16, false>(E, f);
 }
 
-// Blocks of the forward kernel: one while its rows take few turns, then as
-// many as give every group of lanes at least two rows, up to one per SM.
+// Blocks of the forward kernel: one while its rows take up to two turns (its
+// sums then need no second launch), else up to one per SM.
 int route_blocks(int64_t T, int64_t E, int sm_count) {
-  const int lanes = E <= 64 ? 8 : E <= 128 ? 16 : 32;
-  const int64_t rows = kThreads / lanes;
-  const int64_t b = (T + 2 * rows - 1) / (2 * rows);
-  return static_cast<int>(b < 1 ? 1 : b > sm_count ? sm_count : b);
+  const int64_t rows = E <= 64 ? 128 : E <= 128 ? 64 : E <= 256 ? 32 : E <= 512 ? 16 : 8;
+  if (T <= 2 * rows) return 1;
+  const int64_t b = (T + rows - 1) / rows;
+  return static_cast<int>(b > sm_count ? sm_count : b);
 }
 
 template <typename Kernel, typename... Args>
@@ -570,10 +620,12 @@ struct LaunchForward {
   template <typename T, int kLanes, int kVals, bool kSigmoid>
   cudaError_t operator()() {
     a.vec = a.E % kVals == 0;
-    constexpr int kRows = kThreads / kLanes;
-    // 34 KB at most (E = 1024: 8 rows): below the 48 KB that need no opt-in
-    const size_t smem = kRows * 32 * 8 + static_cast<size_t>(a.E) * 4 * (1 + kRows);
-    return launch_pdl(route_kernel<T, kLanes, kVals, kSigmoid>, blocks, kThreads, smem, st, a);
+    constexpr int kBlock = kForward<kVals>;
+    constexpr size_t kChosen = kBlock / kLanes * 32 * 8;
+    constexpr size_t kMax = kChosen + kLanes * kVals * 4 * (1 + kBlock / 32);
+    static_assert(kMax + 1024 <= 48 * 1024, "shared memory without an opt-in");
+    const size_t smem = kChosen + static_cast<size_t>(a.E) * 4 * (1 + kBlock / 32);
+    return launch_pdl(route_kernel<T, kLanes, kVals, kSigmoid>, blocks, kBlock, smem, st, a);
   }
 };
 
