@@ -37,18 +37,6 @@ constexpr int kForward = kVals <= 8 ? 1024 : kVals == 16 ? 512 : 256;
 constexpr int kThreads = 256;  // of the gradient
 constexpr unsigned kFull = 0xffffffffu;
 
-// Logit as a 32-bit key that orders like the float; 0 = never chosen (-inf,
-// NaN).  z + 0 turns -0 into +0 so that the two compare equal.
-__device__ __forceinline__ uint32_t choice_key(float z) {
-  if (!(z > -INFINITY)) return 0u;
-  const uint32_t u = __float_as_uint(z + 0.0f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-__device__ __forceinline__ float key_logit(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
-}
-
 template <int kLanes>
 __device__ __forceinline__ float sum_lanes(float v) {
 #pragma unroll
@@ -56,16 +44,23 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
+// Largest of the lanes of a row (no NaN among them); a whole warp has an
+// instruction for it.
 template <int kLanes>
-__device__ __forceinline__ uint32_t max_lanes(uint32_t v) {
+__device__ __forceinline__ float max_lanes(float v) {
   if constexpr (kLanes == 32) {
-    return __reduce_max_sync(kFull, v);
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
   } else {
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+    for (int o = kLanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
     return v;
   }
 }
+
+// A logit as the choice sees it: NaN, which is never chosen, as -inf.
+__device__ __forceinline__ float choice(float z) { return fmaxf(z, -INFINITY); }
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -130,20 +125,24 @@ __device__ __forceinline__ void store_vals(T* p, int valid, bool vec, const floa
   }
 }
 
-// Sigmoid of z and of -z with one exponential: t = exp(-|z|) <= 1, so neither
-// overflows and 1 - s keeps its digits.
-__device__ __forceinline__ void sigmoid2(float z, float& s, float& not_s) {
-  const float t = __expf(-fabsf(z));
-  const float r = __fdividef(1.0f, 1.0f + t);
-  s = z < 0.0f ? t * r : r;
-  not_s = z < 0.0f ? r : t * r;
+// exp and 1 / x to about two ulp of fp32 in one instruction each, with
+// results below 2^-126 flushed to zero.
+__device__ __forceinline__ float fast_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));  // log2(e)
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// Scores of a row from its logits: e[i] is the score times a factor common to
-// the row (softmax: its denominator; sigmoid: 1, or exp(-m) where every logit
-// is below kFar and scores might underflow), so e / sum is the share.  The
-// many use the fast exponential (off by 2^-22 |z - m| at most); value() of the
-// chosen few the accurate one.
+// Scores of a row from its logits and its largest, `top`: e[i] is the score
+// times a factor common to the row (softmax: its denominator; sigmoid: 1, or
+// exp(-top) where every logit is below kFar and scores might underflow), so
+// e / sum is the share.  The many use the fast exponential (off by at most
+// 2^-22 |z - top|); value() of the chosen few the accurate one.
 constexpr float kFar = -60.0f;
 
 template <int kLanes, int kVals, bool kSigmoid>
@@ -156,21 +155,19 @@ struct RowScores {
     return expf(z - shift);  // below kFar, 1 + exp(z) is 1
   }
 
-  __device__ __forceinline__ RowScores(uint32_t top, const float (&z)[kVals], float (&e)[kVals]) {
-    shift = key_logit(top);
-    far = kSigmoid && shift < kFar;
+  __device__ __forceinline__ RowScores(float top, const float (&z)[kVals], float (&e)[kVals]) {
+    shift = top;
+    far = kSigmoid && top < kFar;
     float s = 0.0f;
+    if (kSigmoid && !far) {
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      float unused;
-      if constexpr (kSigmoid) {
-        sigmoid2(z[i], e[i], unused);
-        if (far) e[i] = __expf(z[i] - shift);
-      } else {
-        e[i] = __expf(z[i] - shift);
-      }
-      s += e[i];
+      for (int i = 0; i < kVals; ++i) e[i] = fast_rcp(1.0f + fast_exp(-z[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) e[i] = fast_exp(z[i] - shift);
     }
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) s += e[i];
     sum = sum_lanes<kLanes>(s);
   }
 };
@@ -197,40 +194,38 @@ __device__ __forceinline__ double loss_slope(float balance, int E, int k, int ro
   return static_cast<double>(balance) * E / (static_cast<double>(k) * n * n);
 }
 
-// A lane's largest key and, as long as `both`, its second largest, with their
-// places (the lower place of two equal keys first).  A lane seldom wins more
-// than one of the k rounds, so the second is at hand when it does, and a scan
-// for more is rare.
+// A lane's largest and second largest key with their indices (the lower index
+// of two equal keys first).  A lane seldom wins more than one of the k rounds,
+// so the second is at hand when it does, and a scan for more is rare: key2 is
+// NaN while it is not known.
 template <int kVals>
 struct Best {
-  uint32_t key, key2;
+  float key, key2;
   int at, at2;
-  bool both;
 
-  // The keys that come after (m, from) in the order of choice.
-  __device__ __forceinline__ void scan(const uint32_t (&k)[kVals], uint32_t m, int from) {
-    key = key2 = 0;
-    at = at2 = 0;
-    both = true;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      const uint32_t v = k[i] < m || (k[i] == m && i > from) ? k[i] : 0u;
-      if (v > key) {
-        key2 = key, at2 = at;
-        key = v, at = i;
-      } else if (v > key2) {
-        key2 = v, at2 = i;
-      }
-    }
+  __device__ __forceinline__ void take(float v, int i) {
+    const bool first = v > key, second = v > key2;
+    key2 = fmaxf(key2, fminf(v, key));
+    at2 = first ? at : second ? i : at2;
+    key = fmaxf(v, key);
+    at = first ? i : at;
   }
 
-  __device__ __forceinline__ void pop(const uint32_t (&k)[kVals]) {
-    if (both) {
-      key = key2, at = at2;
-      both = false;
-    } else {
-      scan(k, key, at);
-    }
+  // Of the keys that come after (m, from) in the order of choice; at0 is the
+  // index of k[0].
+  __device__ __forceinline__ void scan(const float (&k)[kVals], int at0, float m, int from) {
+    key = key2 = -INFINITY;
+    at = at2 = 0;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i)
+      take(k[i] < m || (k[i] == m && at0 + i > from) ? k[i] : -INFINITY, at0 + i);
+  }
+
+  __device__ __forceinline__ Best(const float (&k)[kVals], int at0) {
+    key = key2 = -INFINITY;
+    at = at2 = 0;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) take(k[i], at0 + i);
   }
 };
 
@@ -238,12 +233,10 @@ template <typename T, int kLanes, int kVals, bool kSigmoid>
 __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteArgs a) {
   constexpr int kBlock = kForward<kVals>, kWarps = kBlock / 32;
   constexpr int kRows = kBlock / kLanes;  // rows in flight per block
+  constexpr int kSlots = kMaxTopK / kLanes;  // of the chosen, per lane
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  // [kRows][32] chosen ids and logits, [E] counts, sums [kWarps][E]
-  int* ch_id = reinterpret_cast<int*>(smem_raw);
-  float* ch_z = reinterpret_cast<float*>(ch_id + kRows * 32);
-  int* counts = reinterpret_cast<int*>(ch_z + kRows * 32);
-  float* sums = reinterpret_cast<float*>(counts + a.E);
+  int* counts = reinterpret_cast<int*>(smem_raw);     // [E]
+  float* sums = reinterpret_cast<float*>(counts + a.E);  // [kWarps][E]
   __shared__ int rows_used;
   __shared__ double red[kWarps];
 
@@ -258,8 +251,6 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
   // the lanes of this row group, as bits of the warp
   const unsigned group = kLanes == 32 ? kFull : ((1u << (kLanes % 32)) - 1u) << (lane - l);
   const int first = l * kVals, valid = a.E - first;
-  int* my_id = ch_id + g * 32;
-  float* my_z = ch_z + g * 32;
   float acc[kVals];
 #pragma unroll
   for (int i = 0; i < kVals; ++i) acc[i] = 0.0f;
@@ -271,6 +262,14 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
   for (int turn = 0; turn < turns; ++turn) {
     const int row = (turn * gridDim.x + blockIdx.x) * kRows + g;
     const bool live = row < a.T && (!a.mask || a.mask[row]);
+    if (!__any_sync(kFull, live)) {  // no row of this warp chooses
+      if (row < a.T)
+        for (int j = l; j < a.k; j += kLanes) {
+          a.ids[static_cast<int64_t>(row) * a.k + j] = -1;
+          a.weights[static_cast<int64_t>(row) * a.k + j] = 0.0f;
+        }
+      continue;
+    }
     float z[kVals];
     if (live) {
       load_vals<T, kVals>(static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.E + first,
@@ -279,66 +278,80 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
 #pragma unroll
       for (int i = 0; i < kVals; ++i) z[i] = -INFINITY;
     }
-    uint32_t key[kVals];
+    float key[kVals];
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) key[i] = choice_key(z[i]);
+    for (int i = 0; i < kVals; ++i) key[i] = choice(z[i]);
 
     // k rounds of: the largest key left, in the lowest lane that holds it
-    // (lanes hold rising indices, so that is the lowest index)
-    Best<kVals> best;
-    best.scan(key, 0xffffffffu, -1);
-    uint32_t top = 0;
-    for (int j = 0; j < a.k; ++j) {
-      const uint32_t m = max_lanes<kLanes>(best.key);
-      if (j == 0) top = m;
-      const unsigned holders = __ballot_sync(kFull, best.key == m) & group;
-      if (lane == __ffs(holders) - 1) {
-        my_id[j] = m ? first + best.at : -1;
-        my_z[j] = key_logit(m);
-        if (m) best.pop(key);
+    // (lanes hold rising indices, so that is the lowest index).  Lane l keeps
+    // the slots l, l + kLanes, ...
+    Best<kVals> best(key, first);
+    int id[kSlots];
+    float zc[kSlots];
+    float top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < kSlots; ++t) {
+      id[t] = -1;
+      zc[t] = -INFINITY;
+      const int n = min(a.k - t * kLanes, kLanes);
+#pragma unroll 2
+      for (int j = 0; j < n; ++j) {
+        const float m = max_lanes<kLanes>(best.key);
+        if (t == 0 && j == 0) top = m;
+        unsigned holders = __ballot_sync(kFull, best.key == m);
+        if (kLanes < 32) holders &= group;
+        const int holder = __ffs(holders) - 1;
+        const int won = __shfl_sync(kFull, best.at, holder);
+        if (l == j) id[t] = won, zc[t] = m;
+        if (lane == holder) {
+          best.key = best.key2, best.at = best.at2;
+          best.key2 = __int_as_float(0x7fffffff);
+        }
+        if (best.key != best.key) best.scan(key, first, m, won);
       }
-      __syncwarp();
+      if (!(zc[t] > -INFINITY)) id[t] = -1;  // nothing was left
     }
 
     float e[kVals];
     const RowScores<kLanes, kVals, kSigmoid> sc(top, z, e);
-    const bool used = top != 0;
+    const bool used = top > -INFINITY;
     if (used) {
-      const float inv = 1.0f / sc.sum;
+      const float inv = fast_rcp(sc.sum);
 #pragma unroll
-      for (int i = 0; i < kVals; ++i)
-        if (i < valid) acc[i] += e[i] * inv;
+      for (int i = 0; i < kVals; ++i) acc[i] += e[i] * inv;
       my_rows += l == 0;
     }
     // weights of the chosen
-    float part = 0.0f;
+    float v[kSlots], part = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kSlots; ++t) {
+      v[t] = id[t] >= 0 ? sc.value(zc[t]) : 0.0f;
+      part += v[t];
+    }
+    float factor = a.scale;
     if (a.renorm) {
-      for (int j = l; j < a.k; j += kLanes)
-        if (my_id[j] >= 0) part += sc.value(my_z[j]);
-      part = sum_lanes<kLanes>(part);
+      factor = a.scale / sum_lanes<kLanes>(part);
+      if (sc.sum != sc.sum) factor = sc.sum;  // a NaN logit beside the chosen
+    } else if (!kSigmoid) {
+      factor = a.scale / sc.sum;
     }
     if (row < a.T) {
-      for (int j = l; j < a.k; j += kLanes) {
-        const int id = my_id[j];
+#pragma unroll
+      for (int t = 0; t < kSlots; ++t) {
+        const int j = l + t * kLanes;
+        if (j >= a.k) break;
         float w = 0.0f;
-        if (id >= 0) {
-          if (a.renorm) {
-            w = sc.value(my_z[j]) / part;
-            if (sc.sum != sc.sum) w = sc.sum;  // a NaN logit beside the chosen
-          } else if (kSigmoid) {
-            w = 1.0f / (1.0f + expf(-my_z[j]));
-          } else {
-            w = sc.value(my_z[j]) / sc.sum;
-          }
-          w *= a.scale;
-          atomicAdd(&counts[id], 1);
+        if (id[t] >= 0) {
+          w = v[t] * factor;
+          // a score on its own, not times the row's factor
+          if (kSigmoid && sc.far && !a.renorm) w = expf(zc[t]) * factor;
+          atomicAdd(&counts[id[t]], 1);
         }
         const int64_t o = static_cast<int64_t>(row) * a.k + j;
-        a.ids[o] = id;
+        a.ids[o] = id[t];
         a.weights[o] = w;
       }
     }
-    __syncwarp();
   }
 
   // block sums: the row groups of a warp, then the warps in order
@@ -417,7 +430,7 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThrea
     int c = 0;
     float s = 0.0f;
     if (e < a.E) {
-#pragma unroll 4
+#pragma unroll 10
       for (int b = w; b < blocks; b += kWarps) {
         c += a.part_count[static_cast<int64_t>(b) * a.E + e];
         s += a.part_share[static_cast<int64_t>(b) * a.E + e];
@@ -472,8 +485,9 @@ struct RouteBackArgs {
 // and, for the chosen, the weights' part.  The chosen few are written again
 // over the row's stores by the lane that owns the slot.
 template <typename T, int kLanes, int kVals, bool kSigmoid>
-__global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBackArgs a) {
+__global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_kernel(const RouteBackArgs a) {
   constexpr int kRows = kThreads / kLanes;
+  constexpr int kSlots = kMaxTopK / kLanes;  // of the chosen, per lane
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int g = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
@@ -499,70 +513,74 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
 #pragma unroll
       for (int i = 0; i < kVals; ++i) z[i] = -INFINITY;
     }
-    uint32_t top = 0;
+    // the chosen of this lane's slots, their logits on their way early
+    int id[kSlots];
+    float zc[kSlots], down[kSlots];
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) top = max(top, choice_key(z[i]));
+    for (int t = 0; t < kSlots; ++t) {
+      const int j = l + t * kLanes;
+      id[t] = used && a.d_weights && j < a.k ? a.ids[slot0 + j] : -1;
+      if (id[t] >= a.E) id[t] = -1;
+      down[t] = id[t] >= 0 ? a.d_weights[slot0 + j] * a.scale : 0.0f;
+      zc[t] = id[t] >= 0 ? to_float(zr[id[t]]) : -INFINITY;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) top = fmaxf(top, z[i]);
     top = max_lanes<kLanes>(top);
     float e[kVals];
     const RowScores<kLanes, kVals, kSigmoid> sc(top, z, e);
-    const float inv = 1.0f / sc.sum;
+    const float inv = fast_rcp(sc.sum);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
       e[i] *= inv;  // the share
-      if (i < valid) dot += e[i] * up[i];
+      dot += e[i] * up[i];
     }
     dot = sum_lanes<kLanes>(dot);
 
     // sums over the chosen: part = their scores, mix = score * d_weight
-    float part = 0.0f, mix = 0.0f;
-    if (used && a.d_weights) {
-      for (int j = l; j < a.k; j += kLanes) {
-        const int id = a.ids[slot0 + j];
-        if (id < 0 || id >= a.E) continue;
-        const float v = sc.value(to_float(zr[id]));
-        part += v;
-        mix += v * a.d_weights[slot0 + j];
+    float v[kSlots], part = 0.0f, mix = 0.0f;
+    if (a.d_weights) {
+#pragma unroll
+      for (int t = 0; t < kSlots; ++t) {
+        v[t] = id[t] >= 0 ? sc.value(zc[t]) : 0.0f;
+        part += v[t];
+        mix += v[t] * down[t];
       }
+      part = sum_lanes<kLanes>(part);
+      mix = sum_lanes<kLanes>(mix);
     }
-    part = sum_lanes<kLanes>(part);
-    mix = sum_lanes<kLanes>(mix) * a.scale;
     // softmax without renormalisation: every expert's score loses
     // p_e * sum_j p_j d_w_j; with it, the chosen share `part` instead
-    const bool plain_soft = !kSigmoid && !a.renorm;
-    const float all = dot + (plain_soft ? mix * inv : 0.0f);
-    const float mean = a.renorm ? mix / part : 0.0f;
+    const float all = dot + (!kSigmoid && !a.renorm ? mix * inv : 0.0f);
     if (row < a.T) {
       float d[kVals];
 #pragma unroll
       for (int i = 0; i < kVals; ++i) {
-        float v = e[i] * (up[i] - all);
-        if constexpr (kSigmoid) {
-          float s, not_s;
-          sigmoid2(z[i], s, not_s);
-          v *= not_s;
-        }
-        d[i] = used ? v : 0.0f;
+        float x = e[i] * (up[i] - all);
+        // 1 - s = 1 / (1 + exp(z))
+        if constexpr (kSigmoid) x *= fast_rcp(1.0f + fast_exp(z[i]));
+        d[i] = used ? x : 0.0f;
       }
       store_vals<T, kVals>(dr + first, valid, a.vec, d);
     }
     __syncwarp();
-    if (used && a.d_weights) {
-      for (int j = l; j < a.k; j += kLanes) {
-        const int id = a.ids[slot0 + j];
-        if (id < 0 || id >= a.E) continue;
-        const float zj = to_float(zr[id]);
-        const float v = sc.value(zj), down = a.d_weights[slot0 + j] * a.scale;
-        const float u = a.loss_grad ? a.loss_grad[id] * d_loss : 0.0f;
-        float dz = v * inv * (u - all);
+    if (a.d_weights) {
+      const float per_part = a.renorm ? 1.0f / part : 0.0f, mean = mix * per_part;
+#pragma unroll
+      for (int t = 0; t < kSlots; ++t) {
+        if (id[t] < 0) continue;
+        const float u = a.loss_grad ? a.loss_grad[id[t]] * d_loss : 0.0f;
+        float dz = v[t] * inv * (u - all);
         if (a.renorm)
-          dz += v / part * (down - mean);
+          dz += v[t] * per_part * (down[t] - mean);
         else if (kSigmoid)
-          dz += down / (1.0f + expf(-zj));
+          dz += down[t] * (sc.far ? expf(zc[t]) : v[t]);
         else
-          dz += v * inv * down;
-        if (kSigmoid) dz *= 1.0f / (1.0f + expf(zj));
-        from_float(dr[id], dz);
+          dz += v[t] * inv * down[t];
+        if constexpr (kSigmoid) dz *= fast_rcp(1.0f + fast_exp(zc[t]));
+        from_float(dr[id[t]], dz);
       }
     }
     __syncwarp();
@@ -621,10 +639,9 @@ struct LaunchForward {
   cudaError_t operator()() {
     a.vec = a.E % kVals == 0;
     constexpr int kBlock = kForward<kVals>;
-    constexpr size_t kChosen = kBlock / kLanes * 32 * 8;
-    constexpr size_t kMax = kChosen + kLanes * kVals * 4 * (1 + kBlock / 32);
+    constexpr size_t kMax = kLanes * kVals * 4 * (1 + kBlock / 32);
     static_assert(kMax + 1024 <= 48 * 1024, "shared memory without an opt-in");
-    const size_t smem = kChosen + static_cast<size_t>(a.E) * 4 * (1 + kBlock / 32);
+    const size_t smem = static_cast<size_t>(a.E) * 4 * (1 + kBlock / 32);
     return launch_pdl(route_kernel<T, kLanes, kVals, kSigmoid>, blocks, kBlock, smem, st, a);
   }
 };
