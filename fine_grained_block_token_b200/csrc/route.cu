@@ -141,8 +141,8 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // Scores of a row from its logits and its largest, `top`: e[i] is the score
 // times a factor common to the row (softmax: its denominator; sigmoid: 1, or
 // exp(-top) where every logit is below kFar and scores might underflow), so
-// e / sum is the share.  The many use the fast exponential (off by at most
-// 2^-22 |z - top|); value() of the chosen few the accurate one.
+// e / sum is the share.  The rounding of the exponent's argument puts a score
+// off by 2^-24 |z - top| of itself, the exponential and reciprocal by 2 ulp.
 constexpr float kFar = -60.0f;
 
 template <int kLanes, int kVals, bool kSigmoid>
@@ -151,23 +151,19 @@ struct RowScores {
   bool far;
 
   __device__ __forceinline__ float value(float z) const {
-    if (kSigmoid && !far) return 1.0f / (1.0f + expf(-z));
-    return expf(z - shift);  // below kFar, 1 + exp(z) is 1
+    if (kSigmoid && !far) return fast_rcp(1.0f + fast_exp(-z));
+    return fast_exp(z - shift);  // below kFar, 1 + exp(z) is 1
   }
 
   __device__ __forceinline__ RowScores(float top, const float (&z)[kVals], float (&e)[kVals]) {
     shift = top;
     far = kSigmoid && top < kFar;
     float s = 0.0f;
-    if (kSigmoid && !far) {
 #pragma unroll
-      for (int i = 0; i < kVals; ++i) e[i] = fast_rcp(1.0f + fast_exp(-z[i]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < kVals; ++i) e[i] = fast_exp(z[i] - shift);
+    for (int i = 0; i < kVals; ++i) {
+      e[i] = value(z[i]);
+      s += e[i];
     }
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) s += e[i];
     sum = sum_lanes<kLanes>(s);
   }
 };
@@ -330,10 +326,10 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
     }
     float factor = a.scale;
     if (a.renorm) {
-      factor = a.scale / sum_lanes<kLanes>(part);
+      factor = a.scale * fast_rcp(sum_lanes<kLanes>(part));
       if (sc.sum != sc.sum) factor = sc.sum;  // a NaN logit beside the chosen
     } else if (!kSigmoid) {
-      factor = a.scale / sc.sum;
+      factor = a.scale * fast_rcp(sc.sum);
     }
     if (row < a.T) {
 #pragma unroll
@@ -344,7 +340,7 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
         if (id[t] >= 0) {
           w = v[t] * factor;
           // a score on its own, not times the row's factor
-          if (kSigmoid && sc.far && !a.renorm) w = expf(zc[t]) * factor;
+          if (kSigmoid && sc.far && !a.renorm) w = fast_exp(zc[t]) * factor;
           atomicAdd(&counts[id[t]], 1);
         }
         const int64_t o = static_cast<int64_t>(row) * a.k + j;
@@ -367,7 +363,7 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
   if (my_rows) atomicAdd(&rows_used, my_rows);
   __syncthreads();
   const bool alone = gridDim.x == 1;
-  const double slope = loss_slope(a.balance, a.E, a.k, rows_used);
+  const double slope = alone ? loss_slope(a.balance, a.E, a.k, rows_used) : 0.0;
   double term = 0.0;
   for (int e = threadIdx.x; e < a.E; e += kBlock) {
     float s = 0.0f;
@@ -567,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
     }
     __syncwarp();
     if (a.d_weights) {
-      const float per_part = a.renorm ? 1.0f / part : 0.0f, mean = mix * per_part;
+      const float per_part = a.renorm ? fast_rcp(part) : 0.0f, mean = mix * per_part;
 #pragma unroll
       for (int t = 0; t < kSlots; ++t) {
         if (id[t] < 0) continue;
@@ -576,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
         if (a.renorm)
           dz += v[t] * per_part * (down[t] - mean);
         else if (kSigmoid)
-          dz += down[t] * (sc.far ? expf(zc[t]) : v[t]);
+          dz += down[t] * (sc.far ? fast_exp(zc[t]) : v[t]);
         else
           dz += v[t] * inv * down[t];
         if constexpr (kSigmoid) dz *= fast_rcp(1.0f + fast_exp(zc[t]));
