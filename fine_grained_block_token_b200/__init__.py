@@ -37,5 +37,6 @@ __all__ = [
 def __getattr__(name):
     if name in __all__:
         from . import _binding
-        return getattr(_binding, name)
+        value = globals()[name] = getattr(_binding, name)  # found at once from now on
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -107,8 +107,15 @@ def _ok(status: int, where: str) -> None:
         raise Fp8blError(status, where)
 
 
+try:  # the stream's handle without a Stream object around it (0.1 against 2.4 us a call)
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 def _stream(t: torch.Tensor):
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream(t.get_device())
 
 
 def _ptr(t):
@@ -145,6 +152,9 @@ def _device_of(t, name: str):
 
 
 def _need(t, name: str, dtypes, shape, device) -> None:
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and (shape is None or t.shape == shape)
+            and t.device == device and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -394,6 +404,20 @@ def _out(t, name: str, dtype, shape, device) -> torch.Tensor:
     return t
 
 
+def _scratch(given, device, size, *sizes):
+    """(tensor, address, bytes) of the workspace: the given one (the library
+    checks its size), or a new one of size(*sizes) bytes, which the caller holds
+    until the kernels are enqueued."""
+    if given is None:
+        n = size(*sizes)
+        if n == 0:
+            return None, None, 0
+        given = torch.empty(n, dtype=torch.uint8, device=device)
+    else:
+        _need(given, "workspace", (torch.uint8,), None, device)
+    return given, given.data_ptr(), given.numel()
+
+
 def _route_options(logits, scoring: str):
     dev = _device_of(logits, "logits")
     T, E = _dims2(logits, "logits")
@@ -425,9 +449,9 @@ def route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = True
     counts = _out(counts, "counts", torch.int32, (E,), dev)
     loss = _out(loss, "loss", torch.float32, (1,), dev)
     loss_grad = _out(loss_grad, "loss_grad", torch.float32, (E,), dev)
-    ws, wsb = _workspace(route_workspace_bytes(T, E), dev, workspace)
+    held, ws, wsb = _scratch(workspace, dev, route_workspace_bytes, T, E)
     _ok(_lib.fp8bl_route(_ptr(logits), kind, T, E, top_k, score, renormalize, scale, balance, _ptr(mask),
-                         _ptr(ids), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(loss_grad), _ptr(ws), wsb,
+                         _ptr(ids), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(loss_grad), ws, wsb,
                          _stream(logits)), "fp8bl_route")
     return ids, weights, counts, loss, loss_grad
 
@@ -472,8 +496,8 @@ def group_rows(ids, groups: int, offsets=None, order=None, slot=None, workspace=
     offsets = _out(offsets, "offsets", torch.int32, (groups + 1,), dev)
     order = _out(order, "order", torch.int32, (n,), dev)
     slot = _out(slot, "slot", torch.int32, ids.shape, dev)
-    ws, wsb = _workspace(group_rows_workspace_bytes(n, groups), dev, workspace)
-    _ok(_lib.fp8bl_group_rows(_ptr(ids), n, groups, _ptr(offsets), _ptr(order), _ptr(slot), _ptr(ws), wsb,
+    held, ws, wsb = _scratch(workspace, dev, group_rows_workspace_bytes, n, groups)
+    _ok(_lib.fp8bl_group_rows(_ptr(ids), n, groups, _ptr(offsets), _ptr(order), _ptr(slot), ws, wsb,
                               _stream(ids)), "fp8bl_group_rows")
     return offsets, order, slot
 
@@ -550,9 +574,9 @@ def lora_add(y, x, a, b, offsets, order, scales=None, out=None, workspace=None) 
     if scales is not None:
         _need(scales, "scales", _F32, (L,), dev)
     out = _out(out, "out", torch.bfloat16, (M, N), dev)
-    ws, wsb = _workspace(lora_add_workspace_bytes(M, N, K, R, L), dev, workspace)
+    held, ws, wsb = _scratch(workspace, dev, lora_add_workspace_bytes, M, N, K, R, L)
     _ok(_lib.fp8bl_lora_add(_ptr(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(offsets), _ptr(order), _ptr(y),
-                            _ptr(out), M, N, K, R, L, _ptr(ws), wsb, _stream(x)), "fp8bl_lora_add")
+                            _ptr(out), M, N, K, R, L, ws, wsb, _stream(x)), "fp8bl_lora_add")
     return out
 
 
