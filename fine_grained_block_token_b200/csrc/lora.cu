@@ -72,14 +72,30 @@ __device__ __forceinline__ uint4 ld_y(const void* p) {
   return v;
 }
 
+// Longer batches go to the tiles of lora_tiles.cu.
+constexpr int kSmallM = kThreads;
+
+// The batch's rows in sorted order, on their way together with the offsets
+// (one dependent load less); -1 for rows outside [0, M).  The map's barriers
+// follow.
+__device__ __forceinline__ void load_order(const Args& p, int* order) {
+  const int i = threadIdx.x;
+  if (i < p.M) {
+    const int row = p.order[i];
+    order[i] = row >= 0 && row < p.M ? row : -1;
+  }
+}
+
 // kRT = rank / 16, rounded up to 1, 2, 4 or 8.
 template <int kRT>
 __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const Args p) {
   constexpr int RP = 16 * kRT;
   extern __shared__ __align__(16) float part[];  // [kWarps][kRows][RP]
   __shared__ TileMap map;
+  __shared__ int order[kSmallM];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
+  load_order(p, order);
   map.build<kThreads>(p.offsets, p.M, p.L, kRows);
   const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, q = lane % 4;
@@ -97,8 +113,8 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const Args p) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = h * 8 + g;
-      const int row = r < tile.rows ? p.order[tile.pos + r] : -1;
-      live[h] = row >= 0 && row < p.M;
+      const int row = r < tile.rows ? order[tile.pos + r] : -1;
+      live[h] = row >= 0;
       xp[h] = p.x + static_cast<int64_t>(live[h] ? row : 0) * p.K + q * 8;
     }
     const __nv_bfloat16* ap = p.a + static_cast<int64_t>(tile.group) * p.R * p.K + q * 8;
@@ -145,6 +161,16 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const Args p) {
   }
 }
 
+// Its first product: the accumulator starts from zero.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // One step's operands: 32 columns of B (four n8 tiles) and of y.
 template <int kRT>
 struct Step {
@@ -153,13 +179,19 @@ struct Step {
   uint4 y[2];
 };
 
-template <int kRT>
-__global__ void __launch_bounds__(kThreads) lora_expand_kernel(const Args p) {
+// kExact: the rank is RP itself, so that the strides of B are constants and the
+// addresses of a run of steps differ by immediates.
+template <int kRT, bool kExact>
+__global__ void __launch_bounds__(kThreads, kRT <= 2 ? 2 : 1) lora_expand_kernel(const Args p) {
   constexpr int RP = 16 * kRT;
+  const int R = kExact ? RP : p.R;
   constexpr int kDepth = kRT == 1 ? 4 : kRT == 2 ? 3 : kRT == 4 ? 2 : 1;  // steps loaded ahead
+  constexpr int kRun = kRT == 1 ? 4 : 8;  // neighbouring ranks of a lane
   __shared__ TileMap map;
+  __shared__ int order[kSmallM];
   // The launch before this one is the shrink, whose blocks have all waited
   // for the work before it: offsets, order, B and y are final, u is not yet.
+  load_order(p, order);
   map.build<kThreads>(p.offsets, p.M, p.L, kRows);
   const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
   const int groups = p.L + p.copy_rest;
@@ -176,55 +208,68 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const Args p) {
   while (at < end) {
     const int t = static_cast<int>(at / steps);
     const int s0 = static_cast<int>(at - static_cast<int64_t>(t) * steps);
-    const int s1 = static_cast<int>(end - at < steps - s0 ? s0 + (end - at) : steps);
-    at += s1 - s0;
+    const int n = static_cast<int>(end - at < steps - s0 ? end - at : steps - s0);
+    at += n;
     const Tile tile = map.find(t, groups, kRows);
-    int64_t yo[2];
+    const bool upper = tile.rows > 8;  // any of rows 8 .. 15
+    int64_t yo[2];                     // element of y and out
     bool live[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = h * 8 + g;
-      const int row = r < tile.rows ? p.order[tile.pos + r] : -1;
-      live[h] = row >= 0 && row < p.M;
-      yo[h] = static_cast<int64_t>(row) * p.N + q * 8;
+      const int row = r < tile.rows ? order[tile.pos + r] : -1;
+      live[h] = row >= 0;
+      yo[h] = static_cast<int64_t>(live[h] ? row : 0) * p.N + s0 * 32 + q * 8;
     }
     if (tile.group == p.L) {  // no adapter: out = y
-      for (int s = s0; s < s1; ++s)
-        if (s * 32 + q * 8 < p.N)
+      for (int i = 0; i < n; ++i)
+        if ((s0 + i) * 32 + q * 8 < p.N)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             if (live[h])
-              *reinterpret_cast<uint4*>(p.out + yo[h] + s * 32) = ld_y(p.y + yo[h] + s * 32);
+              *reinterpret_cast<uint4*>(p.out + yo[h] + i * 32) = ld_y(p.y + yo[h] + i * 32);
       continue;
     }
-    const __nv_bfloat16* bp = p.b + static_cast<int64_t>(tile.group) * p.N * p.R;
-    auto load = [&](Step<kRT>& d, int s) {
+    // n index g of n8 tile j is column (g / 2) * 8 + j * 2 + g % 2 of a step
+    const int col = s0 * 32 + (g >> 1) * 8 + (g & 1);
+    const __nv_bfloat16* bp =
+        p.b + (static_cast<int64_t>(tile.group) * p.N + col) * R + q * kRun;
+    const bool rank_in = kExact || q * kRun < R;
+    const bool whole = (s0 + n) * 32 <= p.N;  // no columns past N in this run
+    const __nv_bfloat16* y0 = p.y + yo[0];
+    const __nv_bfloat16* y1 = p.y + yo[1];
+    // Step i (below n), d steps behind the pointers.  What is not loaded keeps
+    // whatever it was: a finite or foreign B past column N meets outputs that
+    // are not stored, and ranks past R stay the zeros of the start.
+    auto load = [&](Step<kRT>& to, int i, int d) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        // n index g of tile j is column (g / 2) * 8 + j * 2 + g % 2
-        const int col = s * 32 + (g >> 1) * 8 + j * 2 + (g & 1);
-        const __nv_bfloat16* br = bp + static_cast<int64_t>(col) * p.R;
-        const bool in = s < s1 && col < p.N;
+        if (!(whole || (s0 + i) * 32 + (g >> 1) * 8 + (g & 1) + 2 * j < p.N)) continue;
+        const __nv_bfloat16* br = bp + (d * 32 + 2 * j) * R;
         if constexpr (kRT == 1) {
-          const uint2 v = in && q * 4 < p.R ? ld_stream8(br + q * 4) : make_uint2(0, 0);
-          d.b[j][0] = v.x, d.b[j][1] = v.y;
+          if (rank_in) {
+            const uint2 v = ld_stream8(br);
+            to.b[j][0] = v.x, to.b[j][1] = v.y;
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < kRT / 2; ++i) {
-            const uint4 v = in && i * 32 + q * 8 < p.R ? ld_stream(br + i * 32 + q * 8)
-                                                       : make_uint4(0, 0, 0, 0);
-            d.b[j][4 * i] = v.x, d.b[j][4 * i + 1] = v.y;
-            d.b[j][4 * i + 2] = v.z, d.b[j][4 * i + 3] = v.w;
-          }
+          for (int k = 0; k < kRT / 2; ++k)
+            if (kExact || k * 32 + q * 8 < R) {
+              const uint4 v = ld_stream(br + k * 32);
+              to.b[j][4 * k] = v.x, to.b[j][4 * k + 1] = v.y;
+              to.b[j][4 * k + 2] = v.z, to.b[j][4 * k + 3] = v.w;
+            }
         }
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (s < s1 && s * 32 + q * 8 < p.N && live[h]) d.y[h] = ld_y(p.y + yo[h] + s * 32);
+      if (whole || (s0 + i) * 32 + q * 8 < p.N) {
+        if (live[0]) to.y[0] = ld_y(y0 + d * 32);
+        if (upper && live[1]) to.y[1] = ld_y(y1 + d * 32);
+      }
     };
-    Step<kRT> buf[kDepth];
+    Step<kRT> buf[kDepth] = {};
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(buf[d], s0 + d);
+    for (int d = 0; d < kDepth; ++d)
+      if (d < n) load(buf[d], d, d);
 
     // u of the tile's rows, summed over the parts of K in order.  Lane (g, q)
     // holds, per 32 ranks, the 8 from 8 q on (with 16 ranks the 4 from 4 q
@@ -242,12 +287,11 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const Args p) {
       const float* up = reinterpret_cast<const float*>(p.u) +
                         static_cast<int64_t>(tile.pos + (r < tile.rows ? r : 0)) * RP;
       const int64_t stride = static_cast<int64_t>(p.M) * RP;
-      constexpr int kRun = kRT == 1 ? 4 : 8;  // neighbouring ranks of a lane
 #pragma unroll
       for (int i = 0; i < (kRT + 1) / 2; ++i) {
         // ranks past R are padding (their u is NaN beside an infinite x)
         float v[kRun] = {};
-        if (r < tile.rows && i * 32 + q * kRun < p.R) {
+        if (r < tile.rows && (kExact || i * 32 + q * kRun < R)) {
 #pragma unroll 4
           for (int c = 0; c < parts; ++c) {
 #pragma unroll
@@ -268,34 +312,42 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const Args p) {
       }
     }
 
-    for (int s = s0; s < s1; s += kDepth) {
+    __nv_bfloat16* o0 = p.out + yo[0];
+    __nv_bfloat16* o1 = p.out + yo[1];
+    for (int i0 = 0; i0 < n; i0 += kDepth) {
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) {
-        if (s + d >= s1) break;  // the same for the whole warp
-        float acc[4][4] = {};
+        const int i = i0 + d;
+        if (i >= n) break;  // the same for the whole warp
+        float acc[4][4];
 #pragma unroll
         for (int f = 0; f < kRT; ++f)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            mma_bf16(acc[j], lo[f][0], lo[f][1], lo[f][2], lo[f][3], buf[d].b[j][2 * f],
-                     buf[d].b[j][2 * f + 1]);
-            mma_bf16(acc[j], hi[f][0], hi[f][1], hi[f][2], hi[f][3], buf[d].b[j][2 * f],
-                     buf[d].b[j][2 * f + 1]);
+            const uint32_t b0 = buf[d].b[j][2 * f], b1 = buf[d].b[j][2 * f + 1];
+            if (f == 0)
+              mma_bf16_first(acc[j], lo[f][0], lo[f][1], lo[f][2], lo[f][3], b0, b1);
+            else
+              mma_bf16(acc[j], lo[f][0], lo[f][1], lo[f][2], lo[f][3], b0, b1);
+            mma_bf16(acc[j], hi[f][0], hi[f][1], hi[f][2], hi[f][3], b0, b1);
           }
-        // accumulator column 2 q + i of tile j is column 8 q + 2 j + i
-        if ((s + d) * 32 + q * 8 < p.N)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (live[h]) {
-              const uint4 v = buf[d].y[h];
-              *reinterpret_cast<uint4*>(p.out + yo[h] + (s + d) * 32) =
-                  make_uint4(lora::add2(v.x, acc[0][2 * h], acc[0][2 * h + 1]),
-                             lora::add2(v.y, acc[1][2 * h], acc[1][2 * h + 1]),
-                             lora::add2(v.z, acc[2][2 * h], acc[2][2 * h + 1]),
-                             lora::add2(v.w, acc[3][2 * h], acc[3][2 * h + 1]));
-            }
-        load(buf[d], s + d + kDepth);
+        // accumulator column 2 q + k of tile j is column 8 q + 2 j + k
+        auto store = [&](__nv_bfloat16* o, const uint4& v, int h) {
+          *reinterpret_cast<uint4*>(o) =
+              make_uint4(lora::add2(v.x, acc[0][2 * h], acc[0][2 * h + 1]),
+                         lora::add2(v.y, acc[1][2 * h], acc[1][2 * h + 1]),
+                         lora::add2(v.z, acc[2][2 * h], acc[2][2 * h + 1]),
+                         lora::add2(v.w, acc[3][2 * h], acc[3][2 * h + 1]));
+        };
+        if (whole || (s0 + i) * 32 + q * 8 < p.N) {
+          if (live[0]) store(o0 + d * 32, buf[d].y[0], 0);
+          if (upper && live[1]) store(o1 + d * 32, buf[d].y[1], 1);
+        }
+        if (i + kDepth < n) load(buf[d], i + kDepth, d + kDepth);
       }
+      bp += kDepth * 32 * R;
+      y0 += kDepth * 32, y1 += kDepth * 32;
+      o0 += kDepth * 32, o1 += kDepth * 32;
     }
   }
   if (!waited) {
@@ -303,9 +355,6 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const Args p) {
     ptx::grid_dep_launch();
   }
 }
-
-// Longer batches go to the tiles of lora_tiles.cu.
-constexpr int64_t kSmallM = 256;
 
 Plan plan_lora(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, int sm_count) {
   if (M > kSmallM) return lora::plan_tiles(M, N, K, R, L, sm_count);
@@ -353,7 +402,8 @@ cudaError_t launch_rank(const Args& a, const Plan& pl, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(lora_shrink_kernel<kRT>, pl.shrink_blocks, smem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(lora_expand_kernel<kRT>, pl.expand_blocks, 0, st, a);
+  return a.R == 16 * kRT ? launch_pdl(lora_expand_kernel<kRT, true>, pl.expand_blocks, 0, st, a)
+                         : launch_pdl(lora_expand_kernel<kRT, false>, pl.expand_blocks, 0, st, a);
 }
 
 }  // namespace
