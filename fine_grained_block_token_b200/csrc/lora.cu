@@ -72,6 +72,10 @@ __device__ __forceinline__ uint4 ld_y(const void* p) {
   return v;
 }
 
+// Parts of K at most: more shorten the shrink, and the expand has to add them
+// up (in one or two batches of loads).
+constexpr int kMaxParts = 8;
+
 // Longer batches go to the tiles of lora_tiles.cu.
 constexpr int kSmallM = kThreads;
 
@@ -120,22 +124,29 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const Args p) {
     const __nv_bfloat16* ap = p.a + static_cast<int64_t>(tile.group) * p.R * p.K + q * 8;
     float acc[2 * kRT][4] = {};
     const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 2
-    for (int s = s0 + w; s < s1; s += kWarps) {
-      const bool in = s * 32 + q * 8 < p.K;
-      uint4 xv[2], av[2 * kRT];
+    // kTogether steps' loads on their way together
+    constexpr int kTogether = kRT == 1 ? 3 : kRT <= 4 ? 2 : 1;
+    for (int s = s0 + w; s < s1; s += kTogether * kWarps) {
+      uint4 xv[kTogether][2], av[kTogether][2 * kRT];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) xv[h] = in && live[h] ? ld_stream(xp[h] + s * 32) : zero;
+      for (int i = 0; i < kTogether; ++i) {
+        const int k = (s + i * kWarps) * 32;
+        const bool in = s + i * kWarps < s1 && k + q * 8 < p.K;
 #pragma unroll
-      for (int n = 0; n < 2 * kRT; ++n) {
-        const int r = n * 8 + g;
-        av[n] = in && r < p.R ? ld_stream(ap + static_cast<int64_t>(r) * p.K + s * 32) : zero;
+        for (int h = 0; h < 2; ++h) xv[i][h] = in && live[h] ? ld_stream(xp[h] + k) : zero;
+#pragma unroll
+        for (int n = 0; n < 2 * kRT; ++n) {
+          const int r = n * 8 + g;
+          av[i][n] = in && r < p.R ? ld_stream(ap + static_cast<int64_t>(r) * p.K + k) : zero;
+        }
       }
 #pragma unroll
-      for (int n = 0; n < 2 * kRT; ++n) {
-        mma_bf16(acc[n], xv[0].x, xv[1].x, xv[0].y, xv[1].y, av[n].x, av[n].y);
-        mma_bf16(acc[n], xv[0].z, xv[1].z, xv[0].w, xv[1].w, av[n].z, av[n].w);
-      }
+      for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+        for (int n = 0; n < 2 * kRT; ++n) {
+          mma_bf16(acc[n], xv[i][0].x, xv[i][1].x, xv[i][0].y, xv[i][1].y, av[i][n].x, av[i][n].y);
+          mma_bf16(acc[n], xv[i][0].z, xv[i][1].z, xv[i][0].w, xv[i][1].w, av[i][n].z, av[i][n].w);
+        }
     }
     // the warps meet in shared memory and are added in their order
     float* mine = part + w * kRows * RP;
@@ -185,8 +196,9 @@ template <int kRT, bool kExact>
 __global__ void __launch_bounds__(kThreads, kRT <= 2 ? 2 : 1) lora_expand_kernel(const Args p) {
   constexpr int RP = 16 * kRT;
   const int R = kExact ? RP : p.R;
-  constexpr int kDepth = kRT == 1 ? 4 : kRT == 2 ? 3 : kRT == 4 ? 2 : 1;  // steps loaded ahead
+  constexpr int kDepth = kRT == 1 ? 4 : kRT <= 4 ? 2 : 1;  // steps loaded ahead
   constexpr int kRun = kRT == 1 ? 4 : 8;  // neighbouring ranks of a lane
+  constexpr int kBatch = kRT <= 2 ? 8 : 4;
   __shared__ TileMap map;
   __shared__ int order[kSmallM];
   // The launch before this one is the shrink, whose blocks have all waited
@@ -197,18 +209,19 @@ __global__ void __launch_bounds__(kThreads, kRT <= 2 ? 2 : 1) lora_expand_kernel
   const int groups = p.L + p.copy_rest;
   const int tiles = map.before[p.L];
   const int parts = lora::parts_of_k(p.shrink_blocks, tiles, p.max_splits);
-  const int steps = (p.N + 31) / 32;
-  const int64_t total = static_cast<int64_t>(map.before[groups]) * steps;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int64_t me = static_cast<int64_t>(threadIdx.x / 32) * gridDim.x + blockIdx.x;
-  int64_t at = total * me / warps;
-  const int64_t end = total * (me + 1) / warps;
+  const uint32_t steps = (p.N + 31) / 32;
+  // this warp's run of steps: an equal share, the first ones one more
+  const uint32_t total = static_cast<uint32_t>(map.before[groups]) * steps;
+  const uint32_t warps = gridDim.x * kWarps;
+  const uint32_t me = threadIdx.x / 32 * gridDim.x + blockIdx.x;
+  const uint32_t share = total / warps, more = total - share * warps;
+  uint32_t at = me * share + (me < more ? me : more);
+  const uint32_t end = at + share + (me < more ? 1 : 0);
   bool waited = false;
 
   while (at < end) {
-    const int t = static_cast<int>(at / steps);
-    const int s0 = static_cast<int>(at - static_cast<int64_t>(t) * steps);
-    const int n = static_cast<int>(end - at < steps - s0 ? end - at : steps - s0);
+    const int t = static_cast<int>(at / steps), s0 = static_cast<int>(at - t * steps);
+    const int n = min(static_cast<int>(end - at), static_cast<int>(steps) - s0);
     at += n;
     const Tile tile = map.find(t, groups, kRows);
     const bool upper = tile.rows > 8;  // any of rows 8 .. 15
@@ -292,14 +305,26 @@ __global__ void __launch_bounds__(kThreads, kRT <= 2 ? 2 : 1) lora_expand_kernel
         // ranks past R are padding (their u is NaN beside an infinite x)
         float v[kRun] = {};
         if (r < tile.rows && (kExact || i * 32 + q * kRun < R)) {
-#pragma unroll 4
-          for (int c = 0; c < parts; ++c) {
+          // a batch of parts on its way before the first is added
 #pragma unroll
-            for (int k = 0; k < kRun; k += 4) {
-              const float4 o =
-                  *reinterpret_cast<const float4*>(up + c * stride + i * 32 + q * kRun + k);
-              v[k] += o.x, v[k + 1] += o.y, v[k + 2] += o.z, v[k + 3] += o.w;
-            }
+          for (int c0 = 0; c0 < kMaxParts; c0 += kBatch) {
+            if (c0 >= parts) break;
+            float4 o[kBatch][kRun / 4];
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+              for (int k = 0; k < kRun / 4; ++k)
+                o[c][k] = c0 + c < parts
+                              ? *reinterpret_cast<const float4*>(up + (c0 + c) * stride + i * 32 +
+                                                                 q * kRun + 4 * k)
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+              for (int k = 0; k < kRun / 4; ++k) {
+                v[4 * k] += o[c][k].x, v[4 * k + 1] += o[c][k].y;
+                v[4 * k + 2] += o[c][k].z, v[4 * k + 3] += o[c][k].w;
+              }
           }
         }
 #pragma unroll
@@ -364,7 +389,7 @@ Plan plan_lora(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, int sm_cou
   const int64_t tiles = M / kRows + (L + 1 < M ? L + 1 : M);
   // a part of K is at least 256 deep: one step of 32 for each warp
   const int64_t parts = (K + 255) / 256;
-  p.max_splits = static_cast<int>(parts < 16 ? parts : 16);
+  p.max_splits = static_cast<int>(parts < kMaxParts ? parts : kMaxParts);
   const int64_t sb = tiles * p.max_splits, eb = (tiles * ((N + 31) / 32) + kWarps - 1) / kWarps;
   // all blocks resident at once: registers allow two per SM, one at the
   // ranks that fill them
