@@ -168,6 +168,24 @@ struct RowScores {
   }
 };
 
+constexpr int kCluster = 8;
+
+// Shared memory of block `rank` of the cluster, at the place of `here`.
+__device__ __forceinline__ int ld_cluster_int(const int* here, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];"
+               : "=r"(v)
+               : "r"(ptx::map_to_cta(ptx::smem_u32(here), rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_double(const double* here, uint32_t rank, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(
+                   ptx::map_to_cta(ptx::smem_u32(here), rank)),
+               "d"(v)
+               : "memory");
+}
+
 struct RouteArgs {
   const void* logits;
   const uint8_t* mask;
@@ -180,6 +198,7 @@ struct RouteArgs {
   int32_t* part_count; // [blocks][E]
   int32_t* part_rows;  // [blocks]
   int T, E, k;
+  int blocks;          // of the forward kernel: up to kCluster are one cluster
   int renorm, vec;
   float scale, balance;
 };
@@ -235,6 +254,7 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
   float* sums = reinterpret_cast<float*>(counts + a.E);  // [kWarps][E]
   __shared__ int rows_used;
   __shared__ double red[kWarps];
+  __shared__ double terms[kCluster];  // of the loss, block 0's copy
 
   for (int e = threadIdx.x; e < a.E; e += kBlock) counts[e] = 0;
   if (threadIdx.x == 0) rows_used = 0;
@@ -362,27 +382,43 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
   }
   if (my_rows) atomicAdd(&rows_used, my_rows);
   __syncthreads();
-  const bool alone = gridDim.x == 1;
-  const double slope = alone ? loss_slope(a.balance, a.E, a.k, rows_used) : 0.0;
-  double term = 0.0;
   for (int e = threadIdx.x; e < a.E; e += kBlock) {
     float s = 0.0f;
     if (want_share)
       for (int w = 0; w < kWarps; ++w) s += sums[w * a.E + e];
-    if (alone) {
-      a.counts[e] = counts[e];
-      if (a.loss_grad) a.loss_grad[e] = static_cast<float>(slope * counts[e]);
-      term += slope * counts[e] * static_cast<double>(s);
+    if (a.blocks <= kCluster) {
+      sums[e] = s;  // this thread alone reads and writes column e
     } else {
       a.part_share[static_cast<int64_t>(blockIdx.x) * a.E + e] = s;
       a.part_count[static_cast<int64_t>(blockIdx.x) * a.E + e] = counts[e];
     }
   }
-  if (!alone) {
+  if (a.blocks > kCluster) {
     if (threadIdx.x == 0) a.part_rows[blockIdx.x] = rows_used;
     return;
   }
-  if (!want_share) return;
+  // One block, or one cluster whose blocks add up a share of the experts each
+  // over all blocks, in order.
+  ptx::cluster_sync();
+  const uint32_t rank = ptx::cluster_ctarank();
+  int rows = 0;
+  for (int b = 0; b < a.blocks; ++b) rows += ld_cluster_int(&rows_used, b);
+  const double slope = loss_slope(a.balance, a.E, a.k, rows);
+  double term = 0.0;
+  const int per = (a.E + a.blocks - 1) / a.blocks;
+  for (int i = threadIdx.x; i < per; i += kBlock) {
+    const int e = static_cast<int>(rank) * per + i;
+    if (e >= a.E) break;
+    int c = 0;
+    double s = 0.0;
+    for (int b = 0; b < a.blocks; ++b) {
+      c += ld_cluster_int(&counts[e], b);
+      s += __int_as_float(ld_cluster_int(reinterpret_cast<const int*>(&sums[e]), b));
+    }
+    a.counts[e] = c;
+    if (a.loss_grad) a.loss_grad[e] = static_cast<float>(slope * c);
+    term += slope * c * s;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(kFull, term, o);
   if (lane == 0) red[threadIdx.x / 32] = term;
@@ -390,6 +426,12 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
   if (threadIdx.x == 0) {
     double t = 0.0;
     for (int w = 0; w < kWarps; ++w) t += red[w];
+    st_cluster_double(&terms[rank], 0, t);
+  }
+  ptx::cluster_sync();  // also: the others have read this block's sums
+  if (rank == 0 && threadIdx.x == 0 && want_share) {
+    double t = 0.0;
+    for (int b = 0; b < a.blocks; ++b) t += terms[b];
     *a.loss = static_cast<float>(t);
   }
 }
@@ -400,8 +442,7 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
 constexpr int kFinalCtas = 8;
 constexpr int kFinalThreads = 512;
 
-__global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThreads)
-    route_final_kernel(const RouteArgs a, int blocks) {
+__global__ void __launch_bounds__(kFinalThreads) route_final_kernel(const RouteArgs a, int blocks) {
   constexpr int kWarps = kFinalThreads / 32;
   __shared__ double terms[kFinalCtas];  // block 0's copy collects
   __shared__ int s_count[kWarps][32];
@@ -449,10 +490,7 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThrea
   if (w == 0) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(kFull, term, o);
-    if (l == 0) {
-      const uint32_t dst = ptx::map_to_cta(ptx::smem_u32(&terms[rank]), 0);
-      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(dst), "d"(term) : "memory");
-    }
+    if (l == 0) st_cluster_double(&terms[rank], 0, term);
   }
   ptx::cluster_sync();
   if (rank == 0 && threadIdx.x == 0) {
@@ -603,27 +641,35 @@ cudaError_t by_type(bool f32, bool sigmoid, int64_t E, F f) {
   return sigmoid ? by_width<__nv_bfloat16, true>(E, f) : by_width<__nv_bfloat16, false>(E, f);
 }
 
-// Blocks of the forward kernel: one while its rows take up to two turns (its
-// sums then need no second launch), else up to one per SM.
+// Blocks of the forward kernel: one while its rows take up to two turns; then
+// one cluster, up to four turns, which adds up its blocks' sums itself; beyond
+// that up to one per SM, and a second launch for the sums.  (4093 x 16 logits:
+// the cluster's four turns take 10 us on the GPU, one turn of 32 blocks and the
+// second launch 8, but that launch costs the host 2.6 us more, and a call
+// by itself is bound by the host.)
 int route_blocks(int64_t T, int64_t E, int sm_count) {
   const int64_t rows = E <= 64 ? 128 : E <= 128 ? 64 : E <= 256 ? 32 : E <= 512 ? 16 : 8;
   if (T <= 2 * rows) return 1;
+  if (T <= 4 * kCluster * rows) return kCluster;
   const int64_t b = (T + rows - 1) / rows;
   return static_cast<int>(b > sm_count ? sm_count : b);
 }
 
 template <typename Kernel, typename... Args>
-cudaError_t launch_pdl(Kernel k, int blocks, int threads, size_t smem, cudaStream_t st,
-                       Args... args) {
+cudaError_t launch_pdl(Kernel k, int blocks, int cluster, int threads, size_t smem,
+                       cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   set_programmatic_serialization(at[0]);
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
@@ -638,7 +684,8 @@ struct LaunchForward {
     constexpr size_t kMax = kLanes * kVals * 4 * (1 + kBlock / 32);
     static_assert(kMax + 1024 <= 48 * 1024, "shared memory without an opt-in");
     const size_t smem = static_cast<size_t>(a.E) * 4 * (1 + kBlock / 32);
-    return launch_pdl(route_kernel<T, kLanes, kVals, kSigmoid>, blocks, kBlock, smem, st, a);
+    return launch_pdl(route_kernel<T, kLanes, kVals, kSigmoid>, blocks,
+                      blocks <= kCluster ? blocks : 1, kBlock, smem, st, a);
   }
 };
 
@@ -652,8 +699,8 @@ struct LaunchBackward {
     constexpr int kRows = kThreads / kLanes;
     const int64_t need = (static_cast<int64_t>(a.T) + kRows - 1) / kRows;
     const int blocks = static_cast<int>(need < sm_count * 8 ? need : sm_count * 8);
-    return launch_pdl(route_backward_kernel<T, kLanes, kVals, kSigmoid>, blocks, kThreads, 0, st,
-                      a);
+    return launch_pdl(route_backward_kernel<T, kLanes, kVals, kSigmoid>, blocks, 1, kThreads, 0,
+                      st, a);
   }
 };
 
@@ -661,7 +708,7 @@ struct LaunchBackward {
 
 size_t route_workspace_bytes(int64_t T, int64_t E, int sm_count) {
   const int b = route_blocks(T, E, sm_count);
-  return b == 1 ? 0 : static_cast<size_t>(b) * (static_cast<size_t>(E) * 8 + 4);
+  return b <= kCluster ? 0 : static_cast<size_t>(b) * (static_cast<size_t>(E) * 8 + 4);
 }
 
 cudaError_t launch_route(const void* logits, bool f32, int64_t T, int64_t E, int64_t k,
@@ -684,12 +731,13 @@ cudaError_t launch_route(const void* logits, bool f32, int64_t T, int64_t E, int
   a.T = static_cast<int>(T);
   a.E = static_cast<int>(E);
   a.k = static_cast<int>(k);
+  a.blocks = blocks;
   a.renorm = renorm;
   a.scale = scale;
   a.balance = balance;
   cudaError_t e = by_type(f32, sigmoid, E, LaunchForward{a, blocks, st});
-  if (e != cudaSuccess || blocks == 1) return e;
-  return launch_pdl(route_final_kernel, kFinalCtas, kFinalThreads, 0, st, a, blocks);
+  if (e != cudaSuccess || blocks <= kCluster) return e;
+  return launch_pdl(route_final_kernel, kFinalCtas, kFinalCtas, kFinalThreads, 0, st, a, blocks);
 }
 
 cudaError_t launch_route_backward(const void* logits, bool f32, const int32_t* ids,

@@ -36,13 +36,14 @@ cudaError_t launch_pdl(Kernel k, int64_t blocks, int threads, size_t smem, cudaS
 // ids outside [0, G) count as group G, behind all others.  Blocks take
 // contiguous pieces of the entries and warps contiguous parts of a piece, so
 // the order within a group is the order of the entries.  Lanes with the same
-// id find one another with a warp match; the first of them adds their number
-// to the warp's own counter, so nothing depends on the order of atomics.
+// id find one another by ballots over the id's bits; the first of them adds
+// their number to the warp's own counter, so nothing depends on the order of
+// atomics.
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortTurns = 8;                              // entries per lane and piece
-constexpr int kPiece = kSortThreads * kSortTurns;          // 4096
+constexpr int kSortTurns = 4;                              // entries per lane and piece
+constexpr int kPiece = kSortThreads * kSortTurns;          // 2048
 constexpr int kMaxSortBlocks = 64;
 constexpr int kKeysPerThread = (kMaxExperts + 1 + kSortThreads - 1) / kSortThreads;  // 3
 
@@ -64,54 +65,101 @@ __global__ void __launch_bounds__(kSortThreads)
     hist[static_cast<int64_t>(blockIdx.x) * (G + 1) + k] = count[k];
 }
 
-// hist == nullptr: this block holds all entries and counts them itself.
+// hist == nullptr: the one block holds all entries in one piece.  Otherwise the
+// launch before this one is the count, whose blocks have all waited for the
+// work before it: ids are final, so the first piece is counted while the
+// count still runs.
 __global__ void __launch_bounds__(kSortThreads)
     group_place_kernel(const int32_t* ids, int n, int G, int per_block, const int32_t* hist,
                        int32_t* offsets, int32_t* order, int32_t* slot) {
-  __shared__ int base[kMaxExperts + 1];
-  __shared__ uint16_t warp_count[kSortWarps][kMaxExperts + 1];  // <= 256 entries per warp
+  __shared__ int base[kMaxExperts + 1];                         // next row of each key
+  __shared__ int total[kMaxExperts + 1];                        // of the piece; first: of all
+  __shared__ uint16_t warp_count[kSortWarps][kMaxExperts + 1];  // <= 128 entries per warp
   __shared__ int scan[kSortWarps];
   const int w = threadIdx.x / 32, l = threadIdx.x % 32;
-  ptx::grid_dep_wait();
-  ptx::grid_dep_launch();
+  const int bits = 32 - __clz(G);  // of a key, 0 .. G
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * per_block;
   const int64_t end = begin + per_block < n ? begin + per_block : n;
+  int key[kSortTurns], rank[kSortTurns];
 
-  // entries per key in all blocks and in the blocks before this one
-  int total[kKeysPerThread], before[kKeysPerThread];
+  // Keys and ranks of a piece's entries: each warp counts its own, then every
+  // key's counts become the counts of the warps before, and total the sum.
+  auto count = [&](int64_t p) {
+    const int64_t at = p + w * (32 * kSortTurns) + l;
+#pragma unroll
+    for (int t = 0; t < kSortTurns; ++t)
+      key[t] = at + t * 32 < end ? group_key(ids[at + t * 32], G) : -1;
+    for (int k = l; k <= G; k += 32) warp_count[w][k] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int t = 0; t < kSortTurns; ++t) {
+      // the lanes that hold the same key, bit by bit (a warp match of 16
+      // warps took ten times as long: 3.3 us for 8 turns)
+      unsigned same = __ballot_sync(kFull, key[t] >= 0);
+      if (key[t] < 0) same = ~same;
+      for (int b = 0; b < bits; ++b) {
+        const bool one = key[t] >> b & 1;
+        const unsigned ones = __ballot_sync(kFull, one);
+        same &= one ? ones : ~ones;
+      }
+      const unsigned earlier = same & ((1u << l) - 1);
+      int seen = 0;
+      if (key[t] >= 0) seen = warp_count[w][key[t]];
+      __syncwarp();
+      rank[t] = seen + __popc(earlier);
+      if (key[t] >= 0 && earlier == 0)
+        warp_count[w][key[t]] = static_cast<uint16_t>(seen + __popc(same));
+      __syncwarp();
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k <= G; k += kSortThreads) {
+      int c[kSortWarps], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kSortWarps; ++i) c[i] = warp_count[i][k];
+#pragma unroll
+      for (int i = 0; i < kSortWarps; ++i) {
+        warp_count[i][k] = static_cast<uint16_t>(sum);
+        sum += c[i];
+      }
+      total[k] = sum;
+    }
+  };
+
+  if (!hist) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+  }
+  count(begin);
+  int before[kKeysPerThread] = {};  // entries of key threadIdx + q * threads in earlier blocks
   if (hist) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
 #pragma unroll
     for (int q = 0; q < kKeysPerThread; ++q) {
-      const int k = threadIdx.x * kKeysPerThread + q;
-      total[q] = before[q] = 0;
-      if (k <= G) {
-#pragma unroll 8
-        for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-          const int c = hist[static_cast<int64_t>(b) * (G + 1) + k];
-          total[q] += c;
-          if (b < static_cast<int>(blockIdx.x)) before[q] += c;
-        }
+      const int k = threadIdx.x + q * kSortThreads;
+      if (k > G) break;
+      int all = 0;
+      const int32_t* h = hist + k;
+#pragma unroll 32
+      for (int b = 0; b < static_cast<int>(gridDim.x); ++b, h += G + 1) {
+        const int c = *h;
+        all += c;
+        if (b < static_cast<int>(blockIdx.x)) before[q] += c;
       }
+      base[k] = all;
     }
   } else {
-    for (int k = threadIdx.x; k <= G; k += kSortThreads) base[k] = 0;
-    __syncthreads();
-    for (int64_t i = begin + threadIdx.x; i < end; i += kSortThreads)
-      atomicAdd(&base[group_key(ids[i], G)], 1);
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kKeysPerThread; ++q) {
-      const int k = threadIdx.x * kKeysPerThread + q;
-      total[q] = k <= G ? base[k] : 0;
-      before[q] = 0;
-    }
-    __syncthreads();
+    for (int k = threadIdx.x; k <= G; k += kSortThreads) base[k] = total[k];
   }
+  __syncthreads();
 
-  // exclusive sums over the keys: a thread owns kKeysPerThread neighbours
+  // exclusive sums over the keys: a thread owns `own` neighbours
+  const int own = (G + kSortThreads) / kSortThreads;
   int mine = 0;
-#pragma unroll
-  for (int q = 0; q < kKeysPerThread; ++q) mine += total[q];
+  for (int q = 0; q < own; ++q) {
+    const int k = threadIdx.x * own + q;
+    if (k <= G) mine += base[k];
+  }
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -121,49 +169,28 @@ __global__ void __launch_bounds__(kSortThreads)
   if (l == 31) scan[w] = incl;
   __syncthreads();
   int start = incl - mine;
-  for (int i = 0; i < w; ++i) start += scan[i];
+#pragma unroll
+  for (int i = 0; i < kSortWarps; ++i)
+    if (i < w) start += scan[i];
+  for (int q = 0; q < own; ++q) {
+    const int k = threadIdx.x * own + q;
+    if (k <= G) {
+      const int c = base[k];
+      base[k] = start;
+      if (blockIdx.x == 0) offsets[k] = start;
+      start += c;
+    }
+  }
+  __syncthreads();
 #pragma unroll
   for (int q = 0; q < kKeysPerThread; ++q) {
-    const int k = threadIdx.x * kKeysPerThread + q;
-    if (k <= G) {
-      base[k] = start + before[q];
-      if (blockIdx.x == 0) offsets[k] = start;
-    }
-    start += total[q];
+    const int k = threadIdx.x + q * kSortThreads;
+    if (k <= G) base[k] += before[q];
   }
   __syncthreads();
 
-  // piece by piece: count per warp, add the earlier warps, place
-  for (int64_t p = begin; p < end; p += kPiece) {
-    for (int i = threadIdx.x; i < kSortWarps * (G + 1); i += kSortThreads)
-      warp_count[i / (G + 1)][i % (G + 1)] = 0;
-    __syncthreads();
-    int key[kSortTurns], rank[kSortTurns];
+  for (int64_t p = begin;;) {
     const int64_t at = p + w * (32 * kSortTurns) + l;
-#pragma unroll
-    for (int t = 0; t < kSortTurns; ++t)
-      key[t] = at + t * 32 < end ? group_key(ids[at + t * 32], G) : -1;
-#pragma unroll
-    for (int t = 0; t < kSortTurns; ++t) {
-      const unsigned same = __match_any_sync(kFull, key[t]);
-      if (key[t] >= 0) rank[t] = warp_count[w][key[t]] + __popc(same & ((1u << l) - 1));
-      __syncwarp();
-      if (key[t] >= 0 && (same & ((1u << l) - 1)) == 0)
-        warp_count[w][key[t]] += static_cast<uint16_t>(__popc(same));
-      __syncwarp();
-    }
-    __syncthreads();
-    // each key: warps' counts become the counts before them, the base moves on
-    for (int k = threadIdx.x; k <= G; k += kSortThreads) {
-      int sum = 0;
-#pragma unroll
-      for (int i = 0; i < kSortWarps; ++i) {
-        const int c = warp_count[i][k];
-        warp_count[i][k] = static_cast<uint16_t>(sum);
-        sum += c;
-      }
-    }
-    __syncthreads();
 #pragma unroll
     for (int t = 0; t < kSortTurns; ++t) {
       if (key[t] >= 0) {
@@ -172,12 +199,12 @@ __global__ void __launch_bounds__(kSortThreads)
         slot[at + t * 32] = key[t] < G ? pos : -1;
       }
     }
-    if (p + kPiece >= end) break;  // the same for the whole block
+    p += kPiece;
+    if (p >= end) break;  // the same for the whole block
     __syncthreads();
-    // the next piece starts behind this one's entries
-#pragma unroll
-    for (int t = 0; t < kSortTurns; ++t)
-      if (key[t] >= 0) atomicAdd(&base[key[t]], 1);
+    for (int k = threadIdx.x; k <= G; k += kSortThreads) base[k] += total[k];
+    __syncthreads();
+    count(p);
     __syncthreads();
   }
 }
