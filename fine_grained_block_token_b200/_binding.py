@@ -140,12 +140,13 @@ _BF16 = (torch.bfloat16,)
 def _device_of(t, name: str):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    index = t.get_device()  # -1 for host tensors
+    if index < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (got {t.device})")
     # the library launches on the current device: a tensor elsewhere would
     # hand another device's pointers to its kernels
     cur = torch.cuda.current_device()
-    if t.device.index != cur:
+    if index != cur:
         raise ValueError(f"{name} is on {t.device} but the current device is cuda:{cur}; "
                          f"call under `with torch.cuda.device({t.device.index}):`")
     return t.device
@@ -450,9 +451,9 @@ def route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = True
     loss = _out(loss, "loss", torch.float32, (1,), dev)
     loss_grad = _out(loss_grad, "loss_grad", torch.float32, (E,), dev)
     held, ws, wsb = _scratch(workspace, dev, route_workspace_bytes, T, E)
-    _ok(_lib.fp8bl_route(_ptr(logits), kind, T, E, top_k, score, renormalize, scale, balance, _ptr(mask),
-                         _ptr(ids), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(loss_grad), ws, wsb,
-                         _stream(logits)), "fp8bl_route")
+    _ok(_lib.fp8bl_route(logits.data_ptr(), kind, T, E, top_k, score, renormalize, scale, balance, _ptr(mask),
+                         ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), loss.data_ptr(),
+                         loss_grad.data_ptr(), ws, wsb, _stream(logits)), "fp8bl_route")
     return ids, weights, counts, loss, loss_grad
 
 
@@ -477,8 +478,8 @@ def route_backward(logits, ids, d_weights=None, loss_grad=None, d_loss=None, sco
     if d_loss is not None:
         _need(d_loss, "d_loss", _F32, (1,), dev)
     d_logits = _out(d_logits, "d_logits", logits.dtype, (T, E), dev)
-    _ok(_lib.fp8bl_route_backward(_ptr(logits), kind, _ptr(ids), _ptr(d_weights), _ptr(loss_grad),
-                                  _ptr(d_loss), T, E, k, score, renormalize, scale, _ptr(d_logits),
+    _ok(_lib.fp8bl_route_backward(logits.data_ptr(), kind, ids.data_ptr(), _ptr(d_weights), _ptr(loss_grad),
+                                  _ptr(d_loss), T, E, k, score, renormalize, scale, d_logits.data_ptr(),
                                   _stream(logits)), "fp8bl_route_backward")
     return d_logits
 
@@ -497,8 +498,8 @@ def group_rows(ids, groups: int, offsets=None, order=None, slot=None, workspace=
     order = _out(order, "order", torch.int32, (n,), dev)
     slot = _out(slot, "slot", torch.int32, ids.shape, dev)
     held, ws, wsb = _scratch(workspace, dev, group_rows_workspace_bytes, n, groups)
-    _ok(_lib.fp8bl_group_rows(_ptr(ids), n, groups, _ptr(offsets), _ptr(order), _ptr(slot), ws, wsb,
-                              _stream(ids)), "fp8bl_group_rows")
+    _ok(_lib.fp8bl_group_rows(ids.data_ptr(), n, groups, offsets.data_ptr(), order.data_ptr(),
+                              slot.data_ptr(), ws, wsb, _stream(ids)), "fp8bl_group_rows")
     return offsets, order, slot
 
 
@@ -526,8 +527,8 @@ def combine_rows(y, weights, slot, base=None, out=None) -> torch.Tensor:
     nothing).  `base` (bf16 [T, H]) may be `out` itself."""
     dev, T, n, k, H = _check_combine(y, weights, slot, "base", base)
     out = _out(out, "out", torch.bfloat16, (T, H), dev)
-    _ok(_lib.fp8bl_combine_rows(_ptr(y), _ptr(weights), _ptr(slot), _ptr(base), _ptr(out), T, n, k, H,
-                                _stream(y)), "fp8bl_combine_rows")
+    _ok(_lib.fp8bl_combine_rows(y.data_ptr(), weights.data_ptr(), slot.data_ptr(), _ptr(base),
+                                out.data_ptr(), T, n, k, H, _stream(y)), "fp8bl_combine_rows")
     return out
 
 
@@ -543,9 +544,9 @@ def combine_rows_backward(d_out, y, weights, slot, offsets, d_y=None, d_weights=
         raise ValueError(f"offsets must be group_rows' [groups + 1], got shape {tuple(offsets.shape)}")
     d_y = _out(d_y, "d_y", torch.bfloat16, (n, H), dev)
     d_weights = _out(d_weights, "d_weights", torch.float32, (T, k), dev)
-    _ok(_lib.fp8bl_combine_rows_backward(_ptr(d_out), _ptr(y), _ptr(weights), _ptr(slot),
-                                         _ptr(offsets) + 4 * (offsets.numel() - 1), _ptr(d_y),
-                                         _ptr(d_weights), T, n, k, H, _stream(y)),
+    _ok(_lib.fp8bl_combine_rows_backward(d_out.data_ptr(), y.data_ptr(), weights.data_ptr(), slot.data_ptr(),
+                                         offsets.data_ptr() + 4 * (offsets.numel() - 1), d_y.data_ptr(),
+                                         d_weights.data_ptr(), T, n, k, H, _stream(y)),
         "fp8bl_combine_rows_backward")
     return d_y, d_weights
 
@@ -575,8 +576,9 @@ def lora_add(y, x, a, b, offsets, order, scales=None, out=None, workspace=None) 
         _need(scales, "scales", _F32, (L,), dev)
     out = _out(out, "out", torch.bfloat16, (M, N), dev)
     held, ws, wsb = _scratch(workspace, dev, lora_add_workspace_bytes, M, N, K, R, L)
-    _ok(_lib.fp8bl_lora_add(_ptr(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(offsets), _ptr(order), _ptr(y),
-                            _ptr(out), M, N, K, R, L, ws, wsb, _stream(x)), "fp8bl_lora_add")
+    _ok(_lib.fp8bl_lora_add(x.data_ptr(), a.data_ptr(), b.data_ptr(), _ptr(scales), offsets.data_ptr(),
+                            order.data_ptr(), y.data_ptr(), out.data_ptr(), M, N, K, R, L, ws, wsb,
+                            _stream(x)), "fp8bl_lora_add")
     return out
 
 

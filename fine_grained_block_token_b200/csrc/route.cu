@@ -159,11 +159,15 @@ struct RowScores {
     shift = top;
     far = kSigmoid && top < kFar;
     float s = 0.0f;
+    if (kSigmoid && !far) {
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      e[i] = value(z[i]);
-      s += e[i];
+      for (int i = 0; i < kVals; ++i) e[i] = fast_rcp(1.0f + fast_exp(-z[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) e[i] = fast_exp(z[i] - shift);
     }
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) s += e[i];
     sum = sum_lanes<kLanes>(s);
   }
 };
