@@ -14,7 +14,8 @@ def _scores(z, scoring):
         e = np.exp(z - z.max())
         p = e / e.sum()
         return p, p
-    s = 1 / (1 + np.exp(-z))
+    with np.errstate(over="ignore"):  # exp(-z) of a far z: a score of 0
+        s = 1 / (1 + np.exp(-z))
     # shares from scores times exp(-m), m = min(max z, 0), so that a row of
     # very small scores still has them
     m = min(z.max(), 0.0)

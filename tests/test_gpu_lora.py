@@ -82,6 +82,16 @@ def test_sizes(fp8, M, N, K, R, L):
     check(fp8, M, N, K, R, L, M + N + K)
 
 
+@pytest.mark.parametrize("M,N,K,R,L", [(256, 136, 328, 128, 256), (256, 96, 2048, 64, 200), (41000, 72, 72, 8, 1),
+                                       (39000, 8, 136, 72, 3)])
+def test_more_tiles_than_blocks(fp8, M, N, K, R, L):
+    """More tiles than the kernels' blocks work on at once."""
+    ids, t = make(M, N, K, R, L, 40)
+    got = run(fp8, t, ids, L)
+    want, slack = bounds(t, ids, K, R)
+    assert (np.abs(np64(got) - want) <= slack).all()
+
+
 @pytest.mark.parametrize("M", [20, 400])
 def test_few_adapters_in_use(fp8, M):
     """Most adapters without rows; every row without an adapter; every row on one."""

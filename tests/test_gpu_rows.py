@@ -98,11 +98,13 @@ def test_route_sizes(fp8, T, E, k, dtype, renorm, scoring):
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
-def test_route_many_rows(fp8, scoring):
-    """More rows than one turn of the grid, an odd number of them, some masked."""
+@pytest.mark.parametrize("T,E", [(9001, 40), (9500, 200), (2049, 1000), (1500, 256)])
+def test_route_many_rows(fp8, T, E, scoring):
+    """One cluster of blocks in several turns, and more rows than one turn of
+    the whole grid; an odd number of them, some masked."""
     g = np.random.default_rng(1)
-    z = logits_of(9001, 40, torch.float32, 5)
-    check_route(fp8, z, 4, scoring, True, mask=g.random(9001) < 0.8, label="many rows")
+    z = logits_of(T, E, torch.float32, 5)
+    check_route(fp8, z, 4, scoring, True, mask=g.random(T) < 0.8, label="many rows")
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
