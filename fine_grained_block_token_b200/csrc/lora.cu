@@ -76,15 +76,32 @@ __device__ __forceinline__ uint4 ld_y(const void* p) {
 // up (in one or two batches of loads).
 constexpr int kMaxParts = 8;
 
-// Longer batches go to the tiles of lora_tiles.cu.
-constexpr int kSmallM = kThreads;
+// Rows that this form can take (their order lies in shared memory).
+constexpr int kSmallM = 2048;
+
+// Whether a batch goes through this form or through the 128-row tiles of
+// lora_tiles.cu.  Here the time grows with the number of 16-row tiles and, as
+// every tile multiplies all of B by 16 rows, with the rank; there every adapter
+// costs at least one 128-row tile.  Both forms, us, beside 28672 x 4096:
+//   rank 16,  1 adapter:    1024 rows 30 | 35     2048 rows  64 | 60
+//   rank 16,  64 adapters:   256 rows 22 | 133    2048 rows  82 | 138
+//   rank 32,  8 adapters:   1024 rows 37 | 37     2048 rows  85 | 67
+//   rank 64,  1 adapter:      64 rows 16 | 17      256 rows  23 | 21
+//   rank 64,  8 adapters:    256 rows 27 | 31      512 rows  36 | 33
+//   rank 128, 1 adapter:      32 rows 21 | 23      256 rows  36 | 27
+//   rank 128, 16 adapters:   256 rows 48 | 75     1024 rows 130 | 79
+bool small_batch(int64_t M, int64_t R, int64_t L) {
+  const int64_t adapters = L < M ? L : M;
+  int64_t most = R <= 32 ? 64 * adapters : R <= 64 ? 128 + 48 * adapters : 32 + 32 * adapters;
+  if (R <= 32 && most < 1024) most = 1024;
+  return M <= most && M <= kSmallM;
+}
 
 // The batch's rows in sorted order, on their way together with the offsets
 // (one dependent load less); -1 for rows outside [0, M).  The map's barriers
 // follow.
 __device__ __forceinline__ void load_order(const Args& p, int* order) {
-  const int i = threadIdx.x;
-  if (i < p.M) {
+  for (int i = threadIdx.x; i < p.M; i += kThreads) {
     const int row = p.order[i];
     order[i] = row >= 0 && row < p.M ? row : -1;
   }
@@ -382,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, kRT <= 2 ? 2 : 1) lora_expand_kernel
 }
 
 Plan plan_lora(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, int sm_count) {
-  if (M > kSmallM) return lora::plan_tiles(M, N, K, R, L, sm_count);
+  if (!small_batch(M, R, L)) return lora::plan_tiles(M, N, K, R, L, sm_count);
   Plan p;
   p.rt = lora::rank_tiles(R);
   // tiles at most: full ones, and one more for each group with rows
@@ -462,7 +479,7 @@ cudaError_t launch_lora_add(const void* x, const void* a, const void* b, const f
   r.shrink_blocks = p.shrink_blocks;
   r.copy_rest = y != out;
   r.err = dev.error_flag;
-  if (M > kSmallM) return lora::launch_tiles(r, p, st);
+  if (!small_batch(M, R, L)) return lora::launch_tiles(r, p, st);
   switch (p.rt) {
     case 1: return launch_rank<1>(r, p, st);
     case 2: return launch_rank<2>(r, p, st);

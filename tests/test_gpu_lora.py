@@ -75,6 +75,12 @@ def test_ranks_and_rows(fp8, M, R):
     check(fp8, M, 264, 136, R, 3, M * 1000 + R)
 
 
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 64, 72, 128])
+@pytest.mark.parametrize("M,L", [(1025, 1), (1100, 3), (2051, 40)])
+def test_ranks_of_long_batches(fp8, M, L, R):
+    check(fp8, M, 200, 328, R, L, M * 1000 + R)
+
+
 @pytest.mark.parametrize("M,N,K,R,L", [(1, 8, 8, 8, 1), (5, 8, 1000, 16, 2), (33, 1000, 8, 32, 4), (64, 4096, 1024, 16, 48),
                                        (512, 72, 2048, 64, 5), (700, 2056, 520, 16, 9), (1000, 136, 264, 128, 2),
                                        (2049, 512, 256, 8, 300), (48, 256, 128, 16, 1024), (1500, 64, 64, 16, 1024)])
@@ -92,7 +98,7 @@ def test_more_tiles_than_blocks(fp8, M, N, K, R, L):
     assert (np.abs(np64(got) - want) <= slack).all()
 
 
-@pytest.mark.parametrize("M", [20, 400])
+@pytest.mark.parametrize("M", [20, 400, 1100])
 def test_few_adapters_in_use(fp8, M):
     """Most adapters without rows; every row without an adapter; every row on one."""
     check(fp8, M, 128, 128, 16, 100, 1, spread=2)
@@ -111,7 +117,7 @@ def test_no_scales_and_no_rows(fp8):
     assert got.shape == (0, 128)
 
 
-@pytest.mark.parametrize("M,R", [(40, 8), (40, 64), (300, 24), (300, 128)])
+@pytest.mark.parametrize("M,R", [(40, 8), (40, 64), (300, 24), (300, 128), (1100, 8), (1100, 32)])
 def test_adapters_and_rows_are_apart(fp8, M, R):
     """NaN and infinities in one adapter, in one row of x or of y stay there."""
     ids, t = make(M, 136, 264, R, 4, 12)
@@ -145,7 +151,7 @@ def test_an_infinite_input_gives_what_the_sum_gives(fp8):
 
 def test_same_bits_alone_and_in_a_batch_again(fp8):
     """The same call twice gives the same bits."""
-    for M in (64, 1000):
+    for M in (64, 1000, 1200):
         ids, t = make(M, 1024, 2048, 32, 6, 21)
         first = run(fp8, t, ids, 6)
         for _ in range(2):
@@ -214,7 +220,7 @@ def test_refusals_on_device(fp8):
     fp8.check()
 
 
-@pytest.mark.parametrize("M", [5, 64, 300])
+@pytest.mark.parametrize("M", [5, 64, 300, 1100])
 def test_beside_the_block_linear(fp8, M):
     """The shared projection and the adapters on top of it, on a side stream and
     as a captured graph that is replayed on new inputs."""
