@@ -2,25 +2,25 @@
 // lora.cu in tiles of 128 sorted rows on the tensor core (tcgen05, bf16 in,
 // fp32 in tensor memory).
 //
-// Shrink, u = x A^T: bound by reading x.  128 threads copy 64-deep slices of
-// the tile's rows (wherever `order` says they are) and of A into a ring of
-// 128-byte-swizzled shared-memory stages with cp.async; one thread issues the
-// MMAs.  K is split over the blocks of a cluster so that all SMs have work;
-// the blocks' sums meet through distributed shared memory, added in the order
-// of the parts, and leave as two bf16 terms side by side ([hi | lo], 2 RP
-// deep).  (Parts that the expand adds up instead cost 38 of 137 us beside
+// Shrink, u = x A^T: bound by reading x.  64-deep slices of the tile's rows and
+// of A come into a ring of 128-byte-swizzled shared-memory stages, by TMA where
+// a full tile's rows are one piece of memory (a request's are), else by cp.async
+// of 128 threads from wherever `order` says; one thread issues the MMAs.  K is
+// split over the blocks of a cluster so that all SMs have work; the blocks'
+// sums meet through distributed shared memory, added in the order of the parts,
+// and leave as two bf16 terms side by side ([hi | lo], 2 RP deep).  (Parts that the expand adds up instead cost 38 of 137 us beside
 // 28672 x 4096 at rank 64 and 4096 rows: every block of the expand read all
 // seven.)
 //
 // Expand, out = y + s u B^T: bound by reading y and writing out.  One
 // accumulation over hi and lo with B read twice multiplies by all 16 bits of
-// u.  Work is
-// numbered in chunks of 64 columns, tile after tile, and every block takes an
-// equal run of chunks.  Of a chunk, B comes by TMA, the MMAs run into one of
-// two halves of tensor memory, and the 128 epilogue threads stream y through
-// a ring of shared-memory slots: cp.async in (8 lanes per 128-byte row
-// piece), add the accumulator row by row (a thread per row, as tensor memory
-// hands it out), write back, and out again in whole row pieces.
+// u.  Work is numbered in chunks of 64 columns, tile after tile, and every block
+// takes an equal run of chunks, or blocks share tiles evenly where that works
+// out.  Of a chunk, B comes by TMA, the MMAs run into one of two halves of
+// tensor memory, and y streams through a ring of shared-memory
+// slots: in by TMA (full tiles of one piece) or cp.async (8 lanes per 128-byte
+// row piece), the accumulator added row by row (a thread per row, as tensor
+// memory hands it out) and written back, and out again the same way.
 //
 // Every wait is bounded; a thread whose wait ran out records the error, stops
 // waiting and runs its loops out (the barriers between threads still match).
@@ -42,6 +42,19 @@ __device__ __forceinline__ void record_error(int* err, int code) { atomicCAS(err
 // Byte offset of 16-byte chunk c of row r in a 128-byte-swizzled block.
 __device__ __forceinline__ uint32_t cell(int r, int c) {
   return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// The tile's first row if its rows follow one another in memory too (a request
+// in one piece), else -1.  Whole warp.
+__device__ __forceinline__ int first_of_run(const Args& p, const Tile& tile) {
+  const int lane = threadIdx.x % 32, first = p.order[tile.pos];
+  bool run = first >= 0 && first + tile.rows <= p.M;
+#pragma unroll
+  for (int i = 0; i < kRows / 32; ++i) {
+    const int r = i * 32 + lane;
+    run = run && (r >= tile.rows || p.order[tile.pos + r] == first + r);
+  }
+  return __all_sync(0xffffffffu, run) ? first : -1;
 }
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
@@ -68,7 +81,9 @@ struct ShrinkShape {
 constexpr int kShrinkThreads = 160;  // 4 copying warps, 1 MMA warp
 
 template <int kRT>
-__global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tiles_kernel(const Args p) {
+__global__ void __launch_bounds__(kShrinkThreads, 2)
+    lora_shrink_tiles_kernel(const __grid_constant__ CUtensorMap tmap_x,
+                             const __grid_constant__ CUtensorMap tmap_a, const Args p) {
   using S = ShrinkShape<kRT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -82,11 +97,13 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tiles_kernel(co
   const int warp = threadIdx.x / 32;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      ptx::mbar_init(full(s), 128);
+      ptx::mbar_init(full(s), 1);
       ptx::mbar_init(empty(s), 1);
     }
     ptx::mbar_init(done, 1);
     ptx::fence_barrier_init();
+    ptx::prefetch_tmap(&tmap_x);
+    ptx::prefetch_tmap(&tmap_a);
   }
   if (warp == 4) {
     ptx::tmem_alloc(ptx::smem_u32(&tmem_holder), S::kTmem);
@@ -112,47 +129,69 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tiles_kernel(co
     const int k0 = static_cast<int>(static_cast<int64_t>(blocks_k) * part / parts);
     const int n = static_cast<int>(static_cast<int64_t>(blocks_k) * (part + 1) / parts) - k0;
     if (warp < 4) {
-      const int c = threadIdx.x % 8, r0 = threadIdx.x / 8;  // chunk and first of 8 rows
-      const __nv_bfloat16* xp[8];
-      unsigned live = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 16 * i;
-        const int row = r < tile.rows ? p.order[tile.pos + r] : -1;
-        const bool in = row >= 0 && row < p.M;
-        live |= static_cast<unsigned>(in) << i;
-        xp[i] = p.x + static_cast<int64_t>(in ? row : 0) * p.K;
-      }
-      const __nv_bfloat16* ap = p.a + static_cast<int64_t>(tile.group) * p.R * p.K;
-      const uint32_t dst0 = cell(r0, c);
-      for (int i = 0; i < n + S::kAhead; ++i) {
-        if (i < n) {
-          const uint32_t u = n_used + i;
-          const int s = u % S::kStages;
-          if (ok && !ptx::mbar_wait(empty(s), ((u / S::kStages) & 1u) ^ 1u)) {
-            record_error(p.err, kErrTimeoutProducer);
-            ok = false;
-          }
-          const uint32_t dst = base + s * S::kStage + dst0;
-          const int k = (k0 + i) * kDeep + c * 8;
-          const bool in = k < p.K;
-          const int ks = in ? k : 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            ptx::cp_async16(dst + j * 2048, xp[j] + ks, in && (live >> j & 1));
-#pragma unroll
-          for (int j = 0; j < kRT; ++j) {
-            const int r = r0 + 16 * j;
-            ptx::cp_async16(dst + kBlock + j * 2048,
-                            ap + static_cast<int64_t>(r < p.R ? r : 0) * p.K + ks, in && r < p.R);
-          }
+      auto wait_empty = [&](uint32_t u) {
+        if (ok && !ptx::mbar_wait(empty(u % S::kStages), ((u / S::kStages) & 1u) ^ 1u)) {
+          record_error(p.err, kErrTimeoutProducer);
+          ok = false;
         }
-        ptx::cp_async_commit();
-        if (i >= S::kAhead) {
-          // the copies of this thread have landed: visible to the tensor core
-          ptx::cp_async_wait<S::kAhead>();
-          ptx::fence_proxy_async_smem();
-          ptx::mbar_arrive(full((n_used + i - S::kAhead) % S::kStages));
+      };
+      const int first = tile.rows == kRows ? first_of_run(p, tile) : -1;
+      if (first >= 0) {
+        // A full tile of rows in one piece: TMA.  It may bring ranks behind R,
+        // of the next adapter: their sums are not used.
+        if (threadIdx.x == 0)
+          for (int i = 0; i < n && ok; ++i) {
+            const uint32_t u = n_used + i;
+            const int s = u % S::kStages, k = (k0 + i) * kDeep * 2;
+            wait_empty(u);
+            if (!ok) break;
+            ptx::mbar_arrive_expect_tx(full(s), S::kStage);
+            ptx::tma_load_2d(base + s * S::kStage, &tmap_x, full(s), k, first);
+            ptx::tma_load_2d(base + s * S::kStage + kBlock, &tmap_a, full(s), k,
+                             tile.group * p.R);
+          }
+        __syncwarp();
+      } else {
+        const int c = threadIdx.x % 8, r0 = threadIdx.x / 8;  // chunk and first of 8 rows
+        const __nv_bfloat16* xp[8];
+        unsigned live = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + 16 * i;
+          const int row = r < tile.rows ? p.order[tile.pos + r] : -1;
+          const bool in = row >= 0 && row < p.M;
+          live |= static_cast<unsigned>(in) << i;
+          xp[i] = p.x + static_cast<int64_t>(in ? row : 0) * p.K;
+        }
+        const __nv_bfloat16* ap = p.a + static_cast<int64_t>(tile.group) * p.R * p.K;
+        const uint32_t dst0 = cell(r0, c);
+        for (int i = 0; i < n + S::kAhead; ++i) {
+          if (i < n) {
+            const uint32_t u = n_used + i;
+            const int s = u % S::kStages;
+            wait_empty(u);
+            const uint32_t dst = base + s * S::kStage + dst0;
+            const int k = (k0 + i) * kDeep + c * 8;
+            const bool in = k < p.K;
+            const int ks = in ? k : 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              ptx::cp_async16(dst + j * 2048, xp[j] + ks, in && (live >> j & 1));
+#pragma unroll
+            for (int j = 0; j < kRT; ++j) {
+              const int r = r0 + 16 * j;
+              ptx::cp_async16(dst + kBlock + j * 2048,
+                              ap + static_cast<int64_t>(r < p.R ? r : 0) * p.K + ks, in && r < p.R);
+            }
+          }
+          ptx::cp_async_commit();
+          if (i >= S::kAhead) {
+            // everyone's copies have landed and are visible to the tensor core
+            ptx::cp_async_wait<S::kAhead>();
+            ptx::fence_proxy_async_smem();
+            ptx::named_barrier_sync(1, 128);
+            if (threadIdx.x == 0) ptx::mbar_arrive(full((n_used + i - S::kAhead) % S::kStages));
+          }
         }
       }
       if (ok && !ptx::mbar_wait(done, item_phase)) {
@@ -250,7 +289,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tiles_kernel(co
 // ----------------------------------------------------------------- expand
 
 constexpr int kCols = 64;            // columns of a chunk
-constexpr int kExpandThreads = 192;  // 4 epilogue warps, 1 MMA warp, 1 TMA warp
+// 4 epilogue warps, one for the copies of B and the MMAs, one for the copies of
+// y and out (with a seventh, registers would be granted as for eight, 128 each)
+constexpr int kMmaWarp = 4, kYWarp = 5, kExpandThreads = 192;
 
 template <int kRT>
 struct ExpandShape {
@@ -271,7 +312,9 @@ struct ExpandShape {
 
 template <int kRT>
 __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
-    lora_expand_tiles_kernel(const __grid_constant__ CUtensorMap tmap_b, const Args p) {
+    lora_expand_tiles_kernel(const __grid_constant__ CUtensorMap tmap_b,
+                             const __grid_constant__ CUtensorMap tmap_y,
+                             const __grid_constant__ CUtensorMap tmap_out, const Args p) {
   using S = ExpandShape<kRT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -279,7 +322,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
   uint8_t* b_s = u_s + S::kUBlocks * kBlock;
   uint8_t* y_s = b_s + S::kBStages * S::kBStage;
   __shared__ TileMap map;
-  __shared__ __align__(8) uint64_t bars[2 * S::kBStages + 5];
+  __shared__ __align__(8) uint64_t bars[2 * S::kBStages + 7 + 2 * S::kSlots];
   __shared__ uint32_t tmem_holder;
   const uint32_t bar0 = ptx::smem_u32(bars);
   auto b_full = [&](int s) { return bar0 + 8u * s; };
@@ -287,6 +330,10 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
   auto t_full = [&](int h) { return bar0 + 8u * (2 * S::kBStages + h); };
   auto t_empty = [&](int h) { return bar0 + 8u * (2 * S::kBStages + 2 + h); };
   const uint32_t u_full = bar0 + 8u * (2 * S::kBStages + 4);
+  const uint32_t run_done = u_full + 8u;  // the epilogue is through with a run's slots
+  auto y_full = [&](int k) { return run_done + 8u * (1 + k); };
+  auto y_ready = [&](int k) { return run_done + 8u * (1 + S::kSlots + k); };  // holds out
+  const uint32_t y_idle = run_done + 8u * (1 + 2 * S::kSlots);  // a full run's slots are stored
   const int warp = threadIdx.x / 32;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kBStages; ++s) {
@@ -298,10 +345,18 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
       ptx::mbar_init(t_empty(h), 128);
     }
     ptx::mbar_init(u_full, 128);
+    ptx::mbar_init(run_done, 1);
+    for (int k = 0; k < S::kSlots; ++k) {
+      ptx::mbar_init(y_full(k), 1);
+      ptx::mbar_init(y_ready(k), 128);
+    }
+    ptx::mbar_init(y_idle, 1);
     ptx::fence_barrier_init();
     ptx::prefetch_tmap(&tmap_b);
+    ptx::prefetch_tmap(&tmap_y);
+    ptx::prefetch_tmap(&tmap_out);
   }
-  if (warp == 4) {
+  if (warp == kMmaWarp) {
     ptx::tmem_alloc(ptx::smem_u32(&tmem_holder), 2 * kCols);
     ptx::tmem_relinquish();
   }
@@ -315,18 +370,42 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
   const int chunks = (p.N + kCols - 1) / kCols;
   const int64_t total = static_cast<int64_t>(map.before[groups]) * chunks;
   int64_t at = total * blockIdx.x / gridDim.x;
-  const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
+  int64_t end = total * (blockIdx.x + 1) / gridDim.x;
+  // Where the tiles go into the blocks with little left over, `team` blocks
+  // share a tile and take its chunks in turn: what they read and write at one
+  // time lies side by side in every row.
+  const int all_tiles = map.before[groups];
+  int team = all_tiles > 0 ? static_cast<int>(gridDim.x) / all_tiles : 0;
+  if (team > chunks) team = chunks;
+  if (10 * static_cast<int64_t>(team) * all_tiles < 9 * static_cast<int64_t>(gridDim.x)) team = 0;
+  if (team > 0) {
+    at = blockIdx.x;
+    end = static_cast<int>(blockIdx.x) < team * all_tiles ? at + 1 : at;
+  }
+  const int every = team > 0 ? team : 1;  // chunks from one of a block to its next
   bool ok = true, waited = false;
   uint32_t n_used = 0;   // chunks multiplied so far: B stage, half of tensor memory
-  uint32_t u_phase = 0;
+  uint32_t u_phase = 0, runs = 0, full_runs = 0;
+  uint32_t b_loads = 0;  // copies of B that were started
+  uint32_t y_used = 0;   // chunks of y that came by TMA: slot and phase
 
   while (at < end) {
-    const int t = static_cast<int>(at / chunks);
-    const int c0 = static_cast<int>(at - static_cast<int64_t>(t) * chunks);
-    const int n = static_cast<int>(end - at < chunks - c0 ? end - at : chunks - c0);
-    at += n;
+    int t, c0, n;
+    if (team > 0) {
+      t = blockIdx.x / team, c0 = blockIdx.x % team;
+      n = (chunks - c0 + team - 1) / team;
+      at = end;
+    } else {
+      t = static_cast<int>(at / chunks);
+      c0 = static_cast<int>(at - static_cast<int64_t>(t) * chunks);
+      n = static_cast<int>(end - at < chunks - c0 ? end - at : chunks - c0);
+      at += n;
+    }
     const Tile tile = map.find(t, groups, kRows);
     const bool rest = tile.group == p.L;  // rows without an adapter: out = y
+    // A full tile of rows in one piece comes and goes by TMA.
+    const int first = rest || tile.rows < kRows ? -1 : first_of_run(p, tile);
+    const bool full = first >= 0;
     if (warp < 4) {
       const int cc = threadIdx.x % 8, r0 = threadIdx.x / 8;  // 16-byte chunk, first of 8 rows
       int64_t off[8];
@@ -342,16 +421,17 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
       const uint32_t mine = cell(r0, cc);
       const int col0 = c0 * kCols + cc * 8;
       auto fetch = [&](int i) {  // y of chunk c0 + i
-        if (i < n && col0 + i * kCols < p.N) {
+        if (i < n && col0 + i * every * kCols < p.N) {
           const uint32_t dst = ptx::smem_u32(y_s) + (i % S::kSlots) * kBlock + mine;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (live >> j & 1) ptx::cp_async16(dst + j * 2048, p.y + off[j] + i * kCols, true);
+            if (live >> j & 1) ptx::cp_async16(dst + j * 2048, p.y + off[j] + i * every * kCols, true);
         }
         ptx::cp_async_commit();
       };
       constexpr int kAhead = S::kSlots - 1;
-      for (int i = 0; i < kAhead; ++i) fetch(i);
+      if (!full)
+        for (int i = 0; i < kAhead; ++i) fetch(i);
 
       if (!waited) {
         ptx::grid_dep_wait();
@@ -377,60 +457,106 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
       }
 
       const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-      for (int i = 0; i < n; ++i) {
-        fetch(i + kAhead);
-        ptx::cp_async_wait<kAhead>();
-        uint8_t* slot = y_s + (i % S::kSlots) * kBlock;
-        if (!rest) {
-          const uint32_t h = (n_used + i) & 1u;
-          if (ok && !ptx::mbar_wait(t_full(h), ((n_used + i) >> 1) & 1u)) {
+      // adds the accumulator of chunk i to this thread's row of a slot
+      auto add = [&](int i, uint8_t* slot) {
+        const uint32_t u = n_used + i, h = u & 1u;
+        if (ok && !ptx::mbar_wait(t_full(h), (u >> 1) & 1u)) {
+          record_error(p.err, kErrTimeoutEpilogue);
+          ok = false;
+        }
+        ptx::tc_fence_after();
+        uint32_t a0[32], a1[32];
+        ptx::tmem_ld_32x32b_x32(lane_base + h * kCols, a0);
+        ptx::tmem_ld_32x32b_x32(lane_base + h * kCols + 32, a1);
+        ptx::tmem_ld_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(t_empty(h));
+        if (!full) ptx::named_barrier_sync(1, 128);  // everyone's y has landed
+        const int r = threadIdx.x;
+        uint4 v[8];  // all reads before the writes that might alias them
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(slot + cell(r, c));
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          auto f = [&](int k) {
+            const int e = c * 8 + k;
+            return __uint_as_float(e < 32 ? a0[e & 31] : a1[e & 31]);
+          };
+          *reinterpret_cast<uint4*>(slot + cell(r, c)) =
+              make_uint4(lora::add2(v[c].x, f(0), f(1)), lora::add2(v[c].y, f(2), f(3)),
+                         lora::add2(v[c].z, f(4), f(5)), lora::add2(v[c].w, f(6), f(7)));
+        }
+      };
+      if (full) {
+        for (int i = 0; i < n; ++i) {
+          const uint32_t v = y_used + i;
+          const int k = v % S::kSlots;
+          if (ok && !ptx::mbar_wait(y_full(k), (v / S::kSlots) & 1u)) {
             record_error(p.err, kErrTimeoutEpilogue);
             ok = false;
           }
-          ptx::tc_fence_after();
-          uint32_t a0[32], a1[32];
-          ptx::tmem_ld_32x32b_x32(lane_base + h * kCols, a0);
-          ptx::tmem_ld_32x32b_x32(lane_base + h * kCols + 32, a1);
-          ptx::tmem_ld_wait();
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(t_empty(h));
-          ptx::named_barrier_sync(1, 128);  // everyone's y has landed
-          const int r = threadIdx.x;
-          uint4 v8[8];  // all reads before the writes that might alias them
-#pragma unroll
-          for (int c = 0; c < 8; ++c) v8[c] = *reinterpret_cast<const uint4*>(slot + cell(r, c));
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint4* q = reinterpret_cast<uint4*>(slot + cell(r, c));
-            const uint4 v = v8[c];
-            auto f = [&](int k) {
-              const int e = c * 8 + k;
-              return __uint_as_float(e < 32 ? a0[e & 31] : a1[e & 31]);
-            };
-            *q = make_uint4(lora::add2(v.x, f(0), f(1)), lora::add2(v.y, f(2), f(3)),
-                            lora::add2(v.z, f(4), f(5)), lora::add2(v.w, f(6), f(7)));
-          }
-          ptx::named_barrier_sync(1, 128);  // the slot holds out
+          add(i, y_s + k * kBlock);
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(y_ready(k));
         }
-        // the cells this thread copied in are the ones it copies out, so the
-        // next copy into the slot needs no barrier
-        if (col0 + i * kCols < p.N) {
-          uint4 o[8];
+        // the next run's plain copies may use any slot
+        if (ok && !ptx::mbar_wait(y_idle, full_runs & 1u)) {
+          record_error(p.err, kErrTimeoutEpilogue);
+          ok = false;
+        }
+      } else {
+        for (int i = 0; i < n; ++i) {
+          fetch(i + kAhead);
+          ptx::cp_async_wait<kAhead>();
+          uint8_t* slot = y_s + (i % S::kSlots) * kBlock;
+          if (!rest) {
+            add(i, slot);
+            ptx::named_barrier_sync(1, 128);  // the slot holds out
+          }
+          // the cells this thread copied in are the ones it copies out, so the
+          // next copy into the slot needs no barrier
+          if (col0 + i * every * kCols < p.N) {
+            uint4 o[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            o[j] = *reinterpret_cast<const uint4*>(slot + mine + j * 2048);
+            for (int j = 0; j < 8; ++j)
+              o[j] = *reinterpret_cast<const uint4*>(slot + mine + j * 2048);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (live >> j & 1) *reinterpret_cast<uint4*>(p.out + off[j] + i * kCols) = o[j];
+            for (int j = 0; j < 8; ++j)
+              if (live >> j & 1) *reinterpret_cast<uint4*>(p.out + off[j] + i * every * kCols) = o[j];
+          }
         }
       }
-    } else if (warp == 4 && !rest) {
+      ptx::named_barrier_sync(1, 128);  // everyone is through with the run
+      if (threadIdx.x == 0) ptx::mbar_arrive(run_done);
+    } else if (warp == kMmaWarp && !rest) {
+      // B of chunk i of the run, into the stage that chunk i - kBStages left
+      auto load_b = [&](int i) {
+        if (i >= n || !ok) return;
+        const uint32_t u = n_used + i;
+        const int s = u % S::kBStages;
+        ok = __all_sync(0xffffffffu,
+                        ptx::mbar_wait(b_empty(s), ((u / S::kBStages) & 1u) ^ 1u));
+        if (!ok) return;
+        if (ptx::elect_one()) {
+          ptx::mbar_arrive_expect_tx(b_full(s), S::kBStage);
+#pragma unroll
+          for (int k = 0; k < S::kBBlocks; ++k)
+            ptx::tma_load_2d(ptx::smem_u32(b_s) + s * S::kBStage + k * kCols * 128, &tmap_b,
+                             b_full(s), k * 128,
+                             tile.group * p.N + (c0 + i * every) * kCols);
+        }
+        __syncwarp();
+        b_loads = u + 1;
+      };
+      for (int i = 0; i < S::kBStages; ++i) load_b(i);
       if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(u_full, u_phase));
       for (int i = 0; i < n && ok; ++i) {
+        // the MMAs of chunk i - 1 are done by now, or soon
+        if (i > 0) load_b(i - 1 + S::kBStages);
         const uint32_t u = n_used + i, h = u & 1u;
         const int s = u % S::kBStages;
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(b_full(s), (u / S::kBStages) & 1u) &&
-                                         ptx::mbar_wait(t_empty(h), ((u >> 1) & 1u) ^ 1u));
+        ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(b_full(s), (u / S::kBStages) & 1u) &&
+                                               ptx::mbar_wait(t_empty(h), ((u >> 1) & 1u) ^ 1u));
         if (!ok) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
@@ -449,21 +575,46 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
         __syncwarp();
       }
       if (!ok && threadIdx.x % 32 == 0) record_error(p.err, kErrTimeoutMma);
-    } else if (warp == 5 && !rest && threadIdx.x % 32 == 0) {
-      for (int i = 0; i < n && ok; ++i) {
-        const uint32_t u = n_used + i;
-        const int s = u % S::kBStages;
-        if (!ptx::mbar_wait(b_empty(s), ((u / S::kBStages) & 1u) ^ 1u)) {
+    } else if (warp == kYWarp && !rest && threadIdx.x % 32 == 0) {
+      // One thread takes a slot from its load to its store and to the next
+      // load.  A run starts when the epilogue is through with the one before:
+      // its slots may be in use by plain copies.  (Rows without an adapter come
+      // last, so every earlier run has passed here, and the phases are waited
+      // for one by one.)
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok && !ptx::mbar_wait(bar, parity)) {
           record_error(p.err, kErrTimeoutProducer);
           ok = false;
-          break;
         }
-        ptx::mbar_arrive_expect_tx(b_full(s), S::kBStage);
-#pragma unroll
-        for (int k = 0; k < S::kBBlocks; ++k)
-          ptx::tma_load_2d(ptx::smem_u32(b_s) + s * S::kBStage + k * kCols * 128, &tmap_b,
-                           b_full(s), k * 128, tile.group * p.N + (c0 + i) * kCols);
+      };
+      if (runs > 0) wait(run_done, (runs - 1) & 1u);
+      if (full && ok) {
+        auto load = [&](int i) {
+          if (i >= n) return;
+          const int k = (y_used + i) % S::kSlots;
+          ptx::mbar_arrive_expect_tx(y_full(k), kBlock);
+          ptx::tma_load_2d(ptx::smem_u32(y_s) + k * kBlock, &tmap_y, y_full(k),
+                           (c0 + i * every) * kCols * 2, first);
+        };
+        for (int i = 0; i < S::kSlots; ++i) load(i);
+        for (int i = 0; i < n && ok; ++i) {
+          const uint32_t v = y_used + i;
+          const int k = v % S::kSlots;
+          wait(y_ready(k), (v / S::kSlots) & 1u);
+          if (!ok) break;
+          ptx::tma_store_2d(&tmap_out, ptx::smem_u32(y_s) + k * kBlock, (c0 + i * every) * kCols * 2,
+                            first);
+          ptx::bulk_commit_group();
+          ptx::bulk_wait_group_read<0>();
+          load(i + S::kSlots);
+        }
+        ptx::mbar_arrive(y_idle);
       }
+    }
+    ++runs;
+    if (full) {
+      ++full_runs;
+      y_used += n;
     }
     if (!rest) {
       n_used += n;
@@ -475,15 +626,22 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
     ptx::grid_dep_launch();
   }
   // What is still on its way when a wait ran out lands before the block ends.
-  if (warp == 5 && threadIdx.x % 32 == 0)
-    for (uint32_t i = 0; i < S::kBStages && i < n_used; ++i) {
-      const uint32_t u = n_used - 1 - i;
+  if (warp == kMmaWarp && threadIdx.x % 32 == 0)
+    for (uint32_t i = 0; i < S::kBStages && i < b_loads; ++i) {
+      const uint32_t u = b_loads - 1 - i;
       if (!ptx::mbar_wait(b_full(u % S::kBStages), (u / S::kBStages) & 1u)) break;
     }
+  if (warp == kYWarp && threadIdx.x % 32 == 0) {
+    for (uint32_t i = 0; i < S::kSlots && i < y_used; ++i) {
+      const uint32_t v = y_used - 1 - i;
+      if (!ptx::mbar_wait(y_full(v % S::kSlots), (v / S::kSlots) & 1u)) break;
+    }
+    ptx::bulk_wait_group<0>();
+  }
   ptx::cp_async_wait<0>();
   ptx::tc_fence_before();
   __syncthreads();  // the epilogue has read what the last MMAs wrote
-  if (warp == 4) ptx::tmem_dealloc(tmem, 2 * kCols);
+  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 2 * kCols);
 }
 
 // ------------------------------------------------------------------- host
@@ -520,15 +678,21 @@ cudaError_t launch_rank(const Args& a, const lora::Plan& pl, cudaStream_t st) {
                                 ExpandShape<kRT>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  CUtensorMap tb;
-  if (!make_tmap_u8(&tb, a.b, static_cast<uint64_t>(a.L) * a.N, static_cast<uint64_t>(a.R) * 2,
-                    kCols, 128))
+  // 128-byte pieces of rows: of x and A along K, of B along the rank, of y and
+  // out along N
+  const uint64_t M = a.M, N = a.N, K = a.K, R = a.R, L = a.L;
+  CUtensorMap tx, ta, tb, ty, to;
+  if (!make_tmap_u8(&tx, a.x, M, K * 2, kRows, 128) ||
+      !make_tmap_u8(&ta, a.a, L * R, K * 2, 16 * kRT, 128) ||
+      !make_tmap_u8(&tb, a.b, L * N, R * 2, kCols, 128) ||
+      !make_tmap_u8(&ty, a.y, M, N * 2, kRows, 128) ||
+      !make_tmap_u8(&to, a.out, M, N * 2, kRows, 128))
     return cudaErrorInvalidValue;
   e = launch_pdl(lora_shrink_tiles_kernel<kRT>, pl.shrink_blocks, kShrinkThreads,
-                 ShrinkShape<kRT>::kSmem, pl.max_splits, st, a);
+                 ShrinkShape<kRT>::kSmem, pl.max_splits, st, tx, ta, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(lora_expand_tiles_kernel<kRT>, pl.expand_blocks, kExpandThreads,
-                    ExpandShape<kRT>::kSmem, 1, st, tb, a);
+                    ExpandShape<kRT>::kSmem, 1, st, tb, ty, to, a);
 }
 
 }  // namespace

@@ -81,6 +81,29 @@ def test_ranks_of_long_batches(fp8, M, L, R):
     check(fp8, M, 200, 328, R, L, M * 1000 + R)
 
 
+@pytest.mark.parametrize("R", [8, 32, 64, 72, 128])
+@pytest.mark.parametrize("M,N,K,lengths", [
+    (3000, 200, 328, [700, 1, 127, 128, 129, 1000, 255]),         # pieces of memory, some full tiles, some not
+    (2500, 1096, 72, [512, 0, 512, 512, 300]),
+    (4100, 72, 1544, [-3, 1024, -5, 1024, 900, 1000])])           # two requests of one adapter, apart
+def test_requests_in_one_piece(fp8, M, N, K, lengths, R):
+    """Requests of consecutive rows, as prompts come: their tiles go another way
+    than scattered rows.  Negative lengths repeat the adapter of the request
+    after next."""
+    L = len(lengths)
+    ids = np.full(M, -1, np.int32)
+    at = 0
+    for l, n in enumerate(lengths):
+        ids[at:at + abs(n) * (100 if n < 0 else 1)] = (l + 2) % L if n < 0 else l
+        at += abs(n) * (100 if n < 0 else 1)
+    _, t = make(M, N, K, R, L, 50 + R)
+    ids = torch.from_numpy(ids)
+    got = run(fp8, t, ids, L)
+    want, slack = bounds(t, ids, K, R)
+    assert (np.abs(np64(got) - want) <= slack).all()
+    assert torch.equal(run(fp8, t, ids, L, out="y"), got)
+
+
 @pytest.mark.parametrize("M,N,K,R,L", [(1, 8, 8, 8, 1), (5, 8, 1000, 16, 2), (33, 1000, 8, 32, 4), (64, 4096, 1024, 16, 48),
                                        (512, 72, 2048, 64, 5), (700, 2056, 520, 16, 9), (1000, 136, 264, 128, 2),
                                        (2049, 512, 256, 8, 300), (48, 256, 128, 16, 1024), (1500, 64, 64, 16, 1024)])
