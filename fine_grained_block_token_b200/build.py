@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8bl.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "gemm_pair.cu", "gemm_ue8m0.cu", "gemm_ue8m0_pair.cu", "gemm_rowwise.cu", "decode.cu", "fused.cu", "noalloc.cu", "route.cu", "rows.cu", "lora.cu", "lora_tiles.cu"]
-HEADERS = ["fp8bl_internal.h", "ptx_sm100.cuh", "quant_math.cuh", "lora_common.cuh"]
+HEADERS = ["fp8bl_internal.h", "ptx_sm100.cuh", "quant_math.cuh", "ptx_bf16.cuh",
+           "lora_common.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include", "fp8bl.h")
 
 

@@ -7,7 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "fp8bl_internal.h"
-#include "ptx_sm100.cuh"
+#include "ptx_bf16.cuh"
 
 namespace fp8bl {
 namespace lora {

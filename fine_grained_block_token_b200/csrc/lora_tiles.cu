@@ -22,6 +22,11 @@
 // row piece), the accumulator added row by row (a thread per row, as tensor
 // memory hands it out) and written back, and out again the same way.
 //
+// 4096 rows of 8 adapters of rank 64 beside 28672 x 4096: 112 to 120 us for
+// 537 MB (73 to 68% of the copy rate): about 15 us of shrink, then 5.5 TB/s of y
+// and out, whose row pieces of 128 bytes lie N apart.  5003 rows at rank 16 beside
+// 4096 x 14336: 60 us for 227 MB, of which the shrink reads 142 MB in 30.
+//
 // Every wait is bounded; a thread whose wait ran out records the error, stops
 // waiting and runs its loops out (the barriers between threads still match).
 #include "lora_common.cuh"
@@ -373,7 +378,8 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
   int64_t end = total * (blockIdx.x + 1) / gridDim.x;
   // Where the tiles go into the blocks with little left over, `team` blocks
   // share a tile and take its chunks in turn: what they read and write at one
-  // time lies side by side in every row.
+  // time lies side by side in every row (112 against 118 us for 4096 rows beside
+  // 28672 x 4096; with 15% of the blocks left over it loses).
   const int all_tiles = map.before[groups];
   int team = all_tiles > 0 ? static_cast<int>(gridDim.x) / all_tiles : 0;
   if (team > chunks) team = chunks;

@@ -39,6 +39,10 @@ cudaError_t launch_pdl(Kernel k, int64_t blocks, int threads, size_t smem, cudaS
 // id find one another by ballots over the id's bits; the first of them adds
 // their number to the warp's own counter, so nothing depends on the order of
 // atomics.
+//
+// Bound by latency, not bytes: one launch up to 2048 entries (64 entries: 3 us
+// on the GPU), two beyond (131072 entries into 256 groups: 10 us, of which the
+// counts of 64 blocks per key and the scattered order are 5).
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -213,7 +217,9 @@ __global__ void __launch_bounds__(kSortThreads)
 //
 // out_t = base_t + sum_j w_tj y[slot_tj], added in the order of j in fp32 and
 // rounded once.  Bound by the bytes of the rows: a thread owns 8 neighbouring
-// columns of one token and has all k rows' 16-byte loads in flight.
+// columns of one token and has all k rows' 16-byte loads in flight (in batches
+// of 8).  4093 tokens x 8 rows of 7168: 82 us, 6.5 TB/s, the copy rate; 32
+// tokens: 3 us on the GPU.
 
 constexpr int kCombineThreads = 128;
 
@@ -222,6 +228,16 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
+  return v;
+}
+
+// base may be out: the plain (coherent) path
+__device__ __forceinline__ uint4 ld_base(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
   return v;
 }
 
@@ -254,7 +270,7 @@ __global__ void __launch_bounds__(kCombineThreads)
   if (v >= vecs) return;
   const int64_t o = static_cast<int64_t>(token) * vecs + v;
   float acc[8] = {};
-  if (base) fma8(acc, ld_stream(base + o), 1.0f);
+  if (base) fma8(acc, ld_base(base + o), 1.0f);
   const int64_t t0 = static_cast<int64_t>(token) * k;
   for (int j0 = 0; j0 < k; j0 += 8) {
     uint4 r[8];
@@ -281,7 +297,8 @@ __global__ void __launch_bounds__(kCombineThreads)
 // Gradient: d_y[slot_tj] = w_tj d_out_t and d_w_tj = <d_out_t, y[slot_tj]>.
 // A block owns a token: d_out_t is read once for its k rows, and the dot
 // products end in one block sum.  Blocks past the tokens write zeros to the
-// rows behind the last one that a slot names (*rows_used .. n).
+// rows behind the last one that a slot names (*rows_used .. n).  2048 tokens x
+// 8 rows of 7168: 83 us, 6.0 TB/s; reads and writes in equal parts bound it.
 constexpr int kBackThreads = 128;
 constexpr int kZeroBlocks = 148;
 
