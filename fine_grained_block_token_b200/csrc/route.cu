@@ -464,14 +464,9 @@ __global__ void __launch_bounds__(kFinalThreads) route_final_kernel(const RouteA
   ptx::grid_dep_launch();
   int rows = 0;
   for (int b = threadIdx.x; b < blocks; b += kFinalThreads) rows += a.part_rows[b];
-  rows = __reduce_add_sync(kFull, rows);
-  if (l == 0) s_rows[w] = rows;
-  __syncthreads();
-  rows = 0;
-  for (int i = 0; i < kWarps; ++i) rows += s_rows[i];
-  const double slope = loss_slope(a.balance, a.E, a.k, rows);
-  double term = 0.0;
-  for (int e0 = static_cast<int>(rank) * 32; e0 < a.E; e0 += kFinalCtas * 32) {
+  double slope = 0.0, term = 0.0;
+  bool first = true;  // the rows are added up with the first experts
+  for (int e0 = static_cast<int>(rank) * 32; first || e0 < a.E; e0 += kFinalCtas * 32) {
     const int e = e0 + l;
     int c = 0;
     float s = 0.0f;
@@ -482,17 +477,29 @@ __global__ void __launch_bounds__(kFinalThreads) route_final_kernel(const RouteA
         s += a.part_share[static_cast<int64_t>(b) * a.E + e];
       }
     }
+    if (first) {
+      rows = __reduce_add_sync(kFull, rows);
+      if (l == 0) s_rows[w] = rows;
+    }
     s_count[w][l] = c;
     s_share[w][l] = s;
     __syncthreads();
-    if (w == 0 && e < a.E) {
-      int ct = 0;
-      double st = 0.0;
-      for (int i = 0; i < kWarps; ++i) ct += s_count[i][l], st += s_share[i][l];
-      a.counts[e] = ct;
-      if (a.loss_grad) a.loss_grad[e] = static_cast<float>(slope * ct);
-      term += slope * ct * st;
+    if (w == 0) {
+      if (first) {
+        rows = __reduce_add_sync(kFull, l < kWarps ? s_rows[l] : 0);
+        slope = loss_slope(a.balance, a.E, a.k, rows);
+      }
+      if (e < a.E) {
+        int ct = 0;
+        double st = 0.0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) ct += s_count[i][l], st += s_share[i][l];
+        a.counts[e] = ct;
+        if (a.loss_grad) a.loss_grad[e] = static_cast<float>(slope * ct);
+        term += slope * ct * st;
+      }
     }
+    first = false;
     __syncthreads();
   }
   if (!a.loss) return;  // the same for every block of the cluster
