@@ -532,6 +532,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
           }
         }
       }
+      ptx::fence_proxy_async_smem();  // the next run's TMA may write any slot
       ptx::named_barrier_sync(1, 128);  // everyone is through with the run
       if (threadIdx.x == 0) ptx::mbar_arrive(run_done);
     } else if (warp == kMmaWarp && !rest) {
