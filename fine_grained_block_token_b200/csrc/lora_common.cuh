@@ -36,6 +36,7 @@ struct Plan {
   int rt;
   int shrink_blocks, expand_blocks;
   int max_splits;
+  int few_clusters = 0;  // both products in one launch of so many clusters
   size_t u_bytes;
 };
 inline int rank_tiles(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }

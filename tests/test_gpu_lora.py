@@ -69,6 +69,15 @@ def check(fp8, M, N, K, R, L, seed, **kw):
     return ids, t, got
 
 
+@pytest.mark.parametrize("M,N,K,R,L", [(1, 28672, 4096, 16, 3), (16, 28672, 136, 16, 64), (9, 40, 14336, 8, 2),
+                                       (1, 5000, 72, 128, 1), (1, 8, 8, 64, 5), (16, 2056, 2048, 16, 1)])
+@pytest.mark.parametrize("bare", [0.0, 0.4, 1.0])
+def test_a_few_rows(fp8, M, N, K, R, L, bare):
+    """Both products in one launch: one cluster and several per tile, more
+    columns than a cluster has warps for, fewer, K shorter than a cluster."""
+    check(fp8, M, N, K, R, L, M + N + K, bare=bare)
+
+
 @pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 64, 72, 128])
 @pytest.mark.parametrize("M", [1, 2, 17, 64, 65, 257, 300])
 def test_ranks_and_rows(fp8, M, R):
