@@ -353,12 +353,11 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
       v[t] = id[t] >= 0 ? sc.value(zc[t]) : 0.0f;
       part += v[t];
     }
-    float factor = a.scale;
     if (a.renorm) {
-      factor = a.scale * fast_rcp(sum_lanes<kLanes>(part));
-      if (sc.sum != sc.sum) factor = sc.sum;  // a NaN logit beside the chosen
-    } else if (!kSigmoid) {
-      factor = a.scale * fast_rcp(sc.sum);
+      part = sum_lanes<kLanes>(part);
+      if (sc.sum != sc.sum) part = sc.sum;  // a NaN logit beside the chosen
+    } else {
+      part = kSigmoid ? 1.0f : sc.sum;
     }
     if (row < a.T) {
 #pragma unroll
@@ -367,9 +366,10 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
         if (j >= a.k) break;
         float w = 0.0f;
         if (id[t] >= 0) {
-          w = v[t] * factor;
+          // divided exactly: the weight of a single chosen expert is `scale`
+          w = a.scale * __fdiv_rn(v[t], part);
           // a score on its own, not times the row's factor
-          if (kSigmoid && sc.far && !a.renorm) w = fast_exp(zc[t]) * factor;
+          if (kSigmoid && sc.far && !a.renorm) w = a.scale * fast_exp(zc[t]);
           atomicAdd(&counts[id[t]], 1);
         }
         const int64_t o = static_cast<int64_t>(row) * a.k + j;
@@ -589,20 +589,26 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
     }
     dot = sum_lanes<kLanes>(dot);
 
-    // sums over the chosen: part = their scores, mix = score * d_weight
+    // The chosen: v their scores or, renormalised, their parts of the sum of
+    // the chosen scores (divided exactly, so that the part of a single one is 1
+    // and its gradient 0), mix = sum of v * d_weight.
     float v[kSlots], part = 0.0f, mix = 0.0f;
     if (a.d_weights) {
 #pragma unroll
       for (int t = 0; t < kSlots; ++t) {
         v[t] = id[t] >= 0 ? sc.value(zc[t]) : 0.0f;
         part += v[t];
+      }
+      if (a.renorm) part = sum_lanes<kLanes>(part);
+#pragma unroll
+      for (int t = 0; t < kSlots; ++t) {
+        if (a.renorm && id[t] >= 0) v[t] = __fdiv_rn(v[t], part);
         mix += v[t] * down[t];
       }
-      part = sum_lanes<kLanes>(part);
       mix = sum_lanes<kLanes>(mix);
     }
     // softmax without renormalisation: every expert's score loses
-    // p_e * sum_j p_j d_w_j; with it, the chosen share `part` instead
+    // p_e * sum_j p_j d_w_j; with it, the chosen share that among themselves
     const float all = dot + (!kSigmoid && !a.renorm ? mix * inv : 0.0f);
     if (row < a.T) {
       float d[kVals];
@@ -617,18 +623,18 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
     }
     __syncwarp();
     if (a.d_weights) {
-      const float per_part = a.renorm ? fast_rcp(part) : 0.0f, mean = mix * per_part;
 #pragma unroll
       for (int t = 0; t < kSlots; ++t) {
         if (id[t] < 0) continue;
         const float u = a.loss_grad ? a.loss_grad[id[t]] * d_loss : 0.0f;
-        float dz = v[t] * inv * (u - all);
+        const float score = sc.value(zc[t]);
+        float dz = score * inv * (u - all);
         if (a.renorm)
-          dz += v[t] * per_part * (down[t] - mean);
+          dz += v[t] * (down[t] - mix);
         else if (kSigmoid)
-          dz += down[t] * (sc.far ? fast_exp(zc[t]) : v[t]);
+          dz += down[t] * (sc.far ? fast_exp(zc[t]) : score);
         else
-          dz += v[t] * inv * down[t];
+          dz += score * inv * down[t];
         if constexpr (kSigmoid) dz *= fast_rcp(1.0f + fast_exp(zc[t]));
         from_float(dr[id[t]], dz);
       }

@@ -159,6 +159,24 @@ def test_route_empty_batch(fp8):
     assert (allmasked[0] == -1).all() and (allmasked[1] == 0).all() and allmasked[3].item() == 0
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("E", [5, 64, 200])
+def test_route_a_single_expert(fp8, E, dtype, scoring):
+    """Renormalised, one chosen expert's weight is `scale` whatever the logits, so
+    nothing comes back through it: the loss's gradient, however small beside
+    d_weights, is all there is."""
+    z = logits_of(300, E, dtype, 77)
+    zd = z.cuda()
+    ids, w, _, _, slope = fp8.route(zd, 1, scoring, True, 2.5, 1e-3)
+    assert (w == 2.5).all()
+    dw = torch.full((300, 1), 3.7, device="cuda")
+    d = fp8.route_backward(zd, ids, dw, slope, None, scoring, True, 2.5)
+    assert torch.equal(d, fp8.route_backward(zd, ids, None, slope, None, scoring, True, 2.5))
+    zero = fp8.route_backward(zd, ids, dw, None, None, scoring, True, 2.5)
+    assert (zero == 0).all()
+
+
 def test_route_parts_of_the_gradient(fp8):
     """Only the weights', only the loss's, neither; and d_loss left out is 1."""
     z = logits_of(37, 48, torch.float32, 9)
