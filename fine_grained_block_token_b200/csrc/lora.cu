@@ -86,7 +86,7 @@ constexpr int kSmallM = 2048;
 
 // Whether both products run in one launch.  On the GPU it takes as long as two,
 // us beside 28672 x 4096: rank 16, 1 row 6.0 | 5.8, 16 rows of 16 adapters 10.7 |
-// 11.1, and saves the host 1.7; at larger ranks the cluster's 64 warps are too
+// 11.1, and saves the host 2 (one row beside 4096 x 4096: 12.8 -> 10.5 a call); at larger ranks the cluster's 64 warps are too
 // few for B: rank 64, 1 row 7.4 | 8.3, but 2 rows 13.5 | 9.8, 16 rows 17 | 12.
 bool few_rows(int64_t M, int64_t R) { return M == 1 || (M <= kRows && R <= 16); }
 

@@ -25,7 +25,7 @@
 // 4096 rows of 8 adapters of rank 64 beside 28672 x 4096: 112 to 120 us for
 // 537 MB (73 to 68% of the copy rate): about 15 us of shrink, then 5.5 TB/s of y
 // and out, whose row pieces of 128 bytes lie N apart.  5003 rows at rank 16 beside
-// 4096 x 14336: 60 us for 227 MB, of which the shrink reads 142 MB in 30.
+// 4096 x 14336: 57 us for 227 MB, of which the shrink reads 142 MB in 27.
 //
 // Every wait is bounded; a thread whose wait ran out records the error, stops
 // waiting and runs its loops out (the barriers between threads still match).
@@ -712,13 +712,18 @@ Plan plan_tiles(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, int sm_co
   const int64_t least = (M + kRows - 1) / kRows, most = M / kRows + (L + 1 < M ? L + 1 : M);
   // Blocks of a cluster: as many as keep the tiles that are likely (full ones
   // and a partial one for each adapter) resident at once, two blocks per SM,
-  // with at least 256 of K each.
+  // with at least 256 of K each.  Sizes between the powers of two pay where
+  // every block still has a long way through K (5003 rows, K = 14336: 6 in place
+  // of 4, 60 -> 57 us; 4096 rows, K = 4096: 7 in place of 4, 121 -> 126) and if the
+  // clusters fit the chip with a margin (47 tiles of 6: 63 -> 78).
   const int64_t likely = least + (L < least ? L : least);
-  // (Clusters of 7 in place of 4 made 36 tiles of K = 4096 slower: 121 -> 126 us.)
   p.max_splits = 1;
   while (p.max_splits < 8 && likely * p.max_splits * 2 <= 2 * sm_count &&
          K >= 512 * static_cast<int64_t>(p.max_splits))
     p.max_splits *= 2;
+  const int64_t between = 2 * sm_count * 92 / 100 / likely;
+  if (between > p.max_splits && between <= 8 && K >= 1536 * between)
+    p.max_splits = static_cast<int>(between);
   const int64_t clusters = 2 * sm_count / p.max_splits;
   p.shrink_blocks = static_cast<int>((most < clusters ? most : clusters) * p.max_splits);
   const int64_t eb = most * ((N + kCols - 1) / kCols), er = sm_count * (p.rt == 8 ? 1 : 2);

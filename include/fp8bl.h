@@ -26,7 +26,8 @@
  *   - All pointers are DEVICE pointers to caller-owned memory on the current
  *     CUDA device; the library never allocates, frees or keeps them.
  *   - All tensors are dense and row-major (last index fastest).
- *   - Every pointer must be 16-byte aligned (fp32 scale arrays: 4-byte).
+ *   - Every pointer must be 16-byte aligned (fp32 scale arrays, and the fp32
+ *     and int32 arrays of the router, row and adapter calls: 4-byte).
  *   - Outputs must not overlap inputs.
  *   - Work is enqueued asynchronously on `stream` (NULL = legacy default
  *     stream); the call returns before the GPU finishes.
@@ -486,7 +487,9 @@ fp8bl_status fp8bl_combine_rows_backward(const void *d_out_bf16, const void *y_b
  *   out_i = y_i + scales_l * (x_i A_l^T) B_l^T,
  * y being the projection's output (of any linear above).  The inner product
  * is kept in fp32 (multiplied as two bf16 terms of 16 significant bits) and
- * out is rounded once.  Rows without an adapter: out_i = y_i.
+ * out is rounded once.  Rows without an adapter: out_i = y_i.  Rows and
+ * adapters do not touch one another: a NaN or an infinity stays in the rows of
+ * its x, y or adapter (an infinity in b makes its column NaN there).
  *
  *   x bf16 in [M, K]     a bf16 in [L, R, K]     b bf16 in [L, N, R]
  *   scales  in : fp32 [L] or NULL (ones)
