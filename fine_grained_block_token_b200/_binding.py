@@ -108,8 +108,10 @@ def _ok(status: int, where: str) -> None:
 
 
 try:  # the stream's handle without a Stream object around it (0.1 against 2.4 us a call)
-    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _current_device
 except ImportError:
+    _current_device = torch.cuda.current_device
+
     def _raw_stream(index: int) -> int:
         return torch.cuda.current_stream(index).cuda_stream
 
@@ -140,12 +142,12 @@ _BF16 = (torch.bfloat16,)
 def _device_of(t, name: str):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    index = t.get_device()  # -1 for host tensors
-    if index < 0 or not t.is_cuda:
+    index = t.get_device() if t.is_cuda else -1
+    if index < 0:
         raise ValueError(f"{name} must be on a CUDA device (got {t.device})")
     # the library launches on the current device: a tensor elsewhere would
     # hand another device's pointers to its kernels
-    cur = torch.cuda.current_device()
+    cur = _current_device()
     if index != cur:
         raise ValueError(f"{name} is on {t.device} but the current device is cuda:{cur}; "
                          f"call under `with torch.cuda.device({t.device.index}):`")
@@ -401,7 +403,9 @@ def _out(t, name: str, dtype, shape, device) -> torch.Tensor:
     """A given output, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, name, (dtype,), shape, device)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _need(t, name, (dtype,), shape, device)
     return t
 
 

@@ -142,6 +142,8 @@ def test_workspace_sizes(lib):
     assert size("fp8bl_route_workspace_bytes", 0, 8) == 0
     assert size("fp8bl_group_rows_workspace_bytes", 0, 8) == 0
     assert size("fp8bl_lora_add_workspace_bytes", 0, 128, 64, 16, 2) == 0
+    assert size("fp8bl_lora_add_workspace_bytes", 16, 4096, 4096, 16, 4) == 0   # one launch
+    assert size("fp8bl_lora_add_workspace_bytes", 64, 4096, 4096, 16, 4) > 0
     assert size("fp8bl_lora_add_workspace_bytes", 64, 100, 64, 16, 2) == 0
     assert size("fp8bl_lora_add_workspace_bytes", 5000, 4096, 14336, 128, 64) <= 64 << 20
 
