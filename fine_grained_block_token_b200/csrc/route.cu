@@ -143,6 +143,17 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
+// With up to 16 experts the gradient's terms cancel to a small rest, and there
+// are few scores to compute: the accurate functions there.
+template <bool kFast>
+__device__ __forceinline__ float exp_of(float x) {
+  return kFast ? fast_exp(x) : expf(x);
+}
+template <bool kFast>
+__device__ __forceinline__ float rcp_of(float x) {
+  return kFast ? fast_rcp(x) : __frcp_rn(x);
+}
+
 // Scores of a row from its logits and its largest, `top`: e[i] is the score
 // times a factor common to the row (softmax: its denominator; sigmoid: 1, or
 // exp(-top) where every logit is below kFar and scores might underflow), so
@@ -152,12 +163,13 @@ constexpr float kFar = -60.0f;
 
 template <int kLanes, int kVals, bool kSigmoid>
 struct RowScores {
+  static constexpr bool kFast = kVals > 2;
   float shift, sum;
   bool far;
 
   __device__ __forceinline__ float value(float z) const {
-    if (kSigmoid && !far) return fast_rcp(1.0f + fast_exp(-z));
-    return fast_exp(z - shift);  // below kFar, 1 + exp(z) is 1
+    if (kSigmoid && !far) return rcp_of<kFast>(1.0f + exp_of<kFast>(-z));
+    return exp_of<kFast>(z - shift);  // below kFar, 1 + exp(z) is 1
   }
 
   __device__ __forceinline__ RowScores(float top, const float (&z)[kVals], float (&e)[kVals]) {
@@ -166,10 +178,10 @@ struct RowScores {
     float s = 0.0f;
     if (kSigmoid && !far) {
 #pragma unroll
-      for (int i = 0; i < kVals; ++i) e[i] = fast_rcp(1.0f + fast_exp(-z[i]));
+      for (int i = 0; i < kVals; ++i) e[i] = rcp_of<kFast>(1.0f + exp_of<kFast>(-z[i]));
     } else {
 #pragma unroll
-      for (int i = 0; i < kVals; ++i) e[i] = fast_exp(z[i] - shift);
+      for (int i = 0; i < kVals; ++i) e[i] = exp_of<kFast>(z[i] - shift);
     }
 #pragma unroll
     for (int i = 0; i < kVals; ++i) s += e[i];
@@ -257,6 +269,7 @@ template <typename T, int kLanes, int kVals, bool kSigmoid>
 __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteArgs a) {
   constexpr int kBlock = kForward<kVals>, kWarps = kBlock / 32;
   constexpr int kRows = kBlock / kLanes;  // rows in flight per block
+  constexpr bool kFast = kVals > 2;
   constexpr int kSlots = kMaxTopK / kLanes;  // of the chosen, per lane
   extern __shared__ __align__(16) unsigned char smem_raw[];
   int* counts = reinterpret_cast<int*>(smem_raw);     // [E]
@@ -341,7 +354,7 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
     const RowScores<kLanes, kVals, kSigmoid> sc(top, z, e);
     const bool used = top > -INFINITY;
     if (used) {
-      const float inv = fast_rcp(sc.sum);
+      const float inv = rcp_of<kFast>(sc.sum);
 #pragma unroll
       for (int i = 0; i < kVals; ++i) acc[i] += e[i] * inv;
       my_rows += l == 0;
@@ -369,7 +382,7 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
           // divided exactly: the weight of a single chosen expert is `scale`
           w = a.scale * __fdiv_rn(v[t], part);
           // a score on its own, not times the row's factor
-          if (kSigmoid && sc.far && !a.renorm) w = a.scale * fast_exp(zc[t]);
+          if (kSigmoid && sc.far && !a.renorm) w = a.scale * exp_of<kFast>(zc[t]);
           atomicAdd(&counts[id[t]], 1);
         }
         const int64_t o = static_cast<int64_t>(row) * a.k + j;
@@ -538,6 +551,7 @@ template <typename T, int kLanes, int kVals, bool kSigmoid>
 __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_kernel(const RouteBackArgs a) {
   constexpr int kRows = kThreads / kLanes;
   constexpr int kSlots = kMaxTopK / kLanes;  // of the chosen, per lane
+  constexpr bool kFast = kVals > 2;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int g = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
@@ -580,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
     top = max_lanes<kLanes>(top);
     float e[kVals];
     const RowScores<kLanes, kVals, kSigmoid> sc(top, z, e);
-    const float inv = fast_rcp(sc.sum);
+    const float inv = rcp_of<kFast>(sc.sum);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
@@ -616,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
       for (int i = 0; i < kVals; ++i) {
         float x = e[i] * (up[i] - all);
         // 1 - s = 1 / (1 + exp(z))
-        if constexpr (kSigmoid) x *= fast_rcp(1.0f + fast_exp(z[i]));
+        if constexpr (kSigmoid) x *= rcp_of<kFast>(1.0f + exp_of<kFast>(z[i]));
         d[i] = used ? x : 0.0f;
       }
       store_vals<T, kVals>(dr + first, valid, a.vec, d);
@@ -632,10 +646,10 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
         if (a.renorm)
           dz += v[t] * (down[t] - mix);
         else if (kSigmoid)
-          dz += down[t] * (sc.far ? fast_exp(zc[t]) : score);
+          dz += down[t] * (sc.far ? exp_of<kFast>(zc[t]) : score);
         else
           dz += score * inv * down[t];
-        if constexpr (kSigmoid) dz *= fast_rcp(1.0f + fast_exp(zc[t]));
+        if constexpr (kSigmoid) dz *= rcp_of<kFast>(1.0f + exp_of<kFast>(zc[t]));
         from_float(dr[id[t]], dz);
       }
     }
@@ -666,7 +680,7 @@ cudaError_t by_type(bool f32, bool sigmoid, int64_t E, F f) {
 // Blocks of the forward kernel: one while its rows take up to two turns; then
 // one cluster, up to four turns, which adds up its blocks' sums itself; beyond
 // that up to one per SM, and a second launch for the sums.  (4093 x 16 logits:
-// the cluster's four turns take 10 us on the GPU, one turn of 32 blocks and the
+// the cluster's four turns take 11 us on the GPU, one turn of 32 blocks and the
 // second launch 8, but that launch costs the host 2.6 us more, and a call
 // by itself is bound by the host.)
 int route_blocks(int64_t T, int64_t E, int sm_count) {
