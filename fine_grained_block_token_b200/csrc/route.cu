@@ -23,7 +23,7 @@
 // What bounds it is the instructions of the choice, not the bytes: with 256
 // experts a row costs about 580 warp instructions, 340 of them apart from the k
 // rounds.  16384 x 256 fp32 logits with 8 of 256: 15 us forward (17 MB), 4 us
-// for the sums of the blocks, 11 us for the gradient; one row: 5.5 us.
+// for the sums of the blocks, 11 us for the gradient; one row: 5.4 us.
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -679,10 +679,10 @@ cudaError_t by_type(bool f32, bool sigmoid, int64_t E, F f) {
 
 // Blocks of the forward kernel: one while its rows take up to two turns; then
 // one cluster, up to four turns, which adds up its blocks' sums itself; beyond
-// that up to one per SM, and a second launch for the sums.  (4093 x 16 logits:
-// the cluster's four turns take 11 us on the GPU, one turn of 32 blocks and the
-// second launch 8, but that launch costs the host 2.6 us more, and a call
-// by itself is bound by the host.)
+// that up to one per SM, and a second launch for the sums.  (16 experts,
+// softmax: the cluster's four turns take 11.0 us on the GPU for 4093 rows, 33
+// blocks and the second launch 6.3 us for 4097, but that launch costs the host
+// 2.6 us more, and a call by itself is bound by the host.)
 int route_blocks(int64_t T, int64_t E, int sm_count) {
   const int64_t rows = E <= 64 ? 128 : E <= 128 ? 64 : E <= 256 ? 32 : E <= 512 ? 16 : 8;
   if (T <= 2 * rows) return 1;
