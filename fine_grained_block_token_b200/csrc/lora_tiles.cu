@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
   const uint32_t run_done = u_full + 8u;  // the epilogue is through with a run's slots
   auto y_full = [&](int k) { return run_done + 8u * (1 + k); };
   auto y_ready = [&](int k) { return run_done + 8u * (1 + S::kSlots + k); };  // holds out
-  const uint32_t y_idle = run_done + 8u * (1 + 2 * S::kSlots);  // a full run's slots are stored
+  // the copies' warp has seen the run before end and stored this run's slots
+  const uint32_t y_idle = run_done + 8u * (1 + 2 * S::kSlots);
   const int warp = threadIdx.x / 32;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kBStages; ++s) {
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
   const int every = team > 0 ? team : 1;  // chunks from one of a block to its next
   bool ok = true, waited = false;
   uint32_t n_used = 0;   // chunks multiplied so far: B stage, half of tensor memory
-  uint32_t u_phase = 0, runs = 0, full_runs = 0;
+  uint32_t u_phase = 0, runs = 0;
   uint32_t b_loads = 0;  // copies of B that were started
   uint32_t y_used = 0;   // chunks of y that came by TMA: slot and phase
 
@@ -505,11 +506,6 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
           ptx::fence_proxy_async_smem();
           ptx::mbar_arrive(y_ready(k));
         }
-        // the next run's plain copies may use any slot
-        if (ok && !ptx::mbar_wait(y_idle, full_runs & 1u)) {
-          record_error(p.err, kErrTimeoutEpilogue);
-          ok = false;
-        }
       } else {
         for (int i = 0; i < n; ++i) {
           fetch(i + kAhead);
@@ -531,6 +527,12 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
               if (live >> j & 1) *reinterpret_cast<uint4*>(p.out + off[j] + i * every * kCols) = o[j];
           }
         }
+      }
+      // The next run's plain copies may use any slot.  After every run, so that
+      // run_done is at most one phase ahead of the warp that waits for it.
+      if (!rest && ok && !ptx::mbar_wait(y_idle, runs & 1u)) {
+        record_error(p.err, kErrTimeoutEpilogue);
+        ok = false;
       }
       ptx::fence_proxy_async_smem();  // the next run's TMA may write any slot
       ptx::named_barrier_sync(1, 128);  // everyone is through with the run
@@ -587,7 +589,8 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
       // load.  A run starts when the epilogue is through with the one before:
       // its slots may be in use by plain copies.  (Rows without an adapter come
       // last, so every earlier run has passed here, and the phases are waited
-      // for one by one.)
+      // for one by one: the epilogue does not end a run before this thread has
+      // seen the end of the one before.)
       auto wait = [&](uint32_t bar, uint32_t parity) {
         if (ok && !ptx::mbar_wait(bar, parity)) {
           record_error(p.err, kErrTimeoutProducer);
@@ -615,14 +618,11 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandShape<kRT>::kMinBlocks)
           ptx::bulk_wait_group_read<0>();
           load(i + S::kSlots);
         }
-        ptx::mbar_arrive(y_idle);
       }
+      ptx::mbar_arrive(y_idle);
     }
     ++runs;
-    if (full) {
-      ++full_runs;
-      y_used += n;
-    }
+    if (full) y_used += n;
     if (!rest) {
       n_used += n;
       u_phase ^= 1;

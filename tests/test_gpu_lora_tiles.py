@@ -1,0 +1,89 @@
+"""The long form of the adapters (lora_add) where a block or a cluster goes on
+from one 128-row tile to the next: full tiles of consecutive rows, which come
+and go by TMA, full tiles of scattered rows and partial ones, which do not, in
+every order.  Every case first works out, from the tiles and the launch sizes,
+which steps it takes, and asserts that they are the ones it is there for.
+
+Tolerance: as derived for the other tests of lora_add."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_lora import bounds, make, np64, run
+
+pytestmark = pytest.mark.gpu
+ROWS, COLS = 128, 64    # of a tile, of the expand's chunks
+
+
+@pytest.fixture(scope="module")
+def fp8():
+    import fine_grained_block_token_b200 as m
+    return m
+
+
+def requests(lengths, adapters, scattered=()):
+    """Rows of consecutive requests, adapter i % adapters each; two requests in
+    `scattered` share their rows in turn."""
+    ids = np.concatenate([np.full(n, i % adapters) for i, n in enumerate(lengths)]).astype(np.int32)
+    start = np.concatenate([[0], np.cumsum(lengths)])
+    for i, j in scattered:
+        at = np.r_[start[i]:start[i + 1], start[j]:start[j + 1]]
+        ids[at[::2]], ids[at[1::2]] = i % adapters, j % adapters
+    return ids
+
+
+def tiles_of(ids, L):
+    """'T' for a full tile of consecutive rows, 'F' for a full one of scattered
+    rows, 'P' for a partial one, in the order of the kernels' tile numbers."""
+    out = []
+    for l in range(L):
+        rows = np.nonzero(ids == l)[0]
+        for t in range(0, rows.size, ROWS):
+            r = rows[t:t + ROWS]
+            out.append("P" if r.size < ROWS else "T" if r[-1] - r[0] == ROWS - 1 else "F")
+    return out
+
+
+def expand_steps(kinds, N, R):
+    """The steps from one tile to the next that the expand's blocks take
+    (every adapter's tiles, in place: no rows to copy)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    blocks, chunks = sms * (1 if R > 64 else 2), -(-N // COLS)
+    total = len(kinds) * chunks
+    blocks = min(blocks, total)
+    team = min(blocks // len(kinds), chunks)
+    if 10 * team * len(kinds) >= 9 * blocks:
+        return set()
+    steps = set()
+    for b in range(blocks):
+        lo, hi = total * b // blocks, total * (b + 1) // blocks
+        mine = [kinds[t] for t in range(lo // chunks, -(-hi // chunks))] if hi > lo else []
+        steps |= {a + b for a, b in zip(mine, mine[1:])}
+    return steps
+
+
+def compare(fp8, ids, t, K, R, L):
+    ids = torch.from_numpy(ids)
+    got = run(fp8, t, ids, L)
+    want, slack = bounds(t, ids, K, R)
+    bad = ~(np.abs(np64(got) - want) <= slack)
+    assert not bad.any(), (int(bad.sum()), np.unique(np.nonzero(bad)[0] // ROWS)[:10])
+    for _ in range(2):
+        assert torch.equal(run(fp8, t, ids, L, out="y"), got)
+
+
+@pytest.mark.parametrize("R", [8, 32, 64, 72, 128])
+@pytest.mark.parametrize("N", [136, 584])
+def test_expand_goes_from_tile_to_tile(fp8, N, R):
+    """Blocks of the expand with several runs: the copies' warp hands its slots
+    over between every pair of kinds.  One tile for every cluster of the shrink."""
+    K, L = 72, 12
+    g = np.random.default_rng(R)
+    lengths = [int(n) for n in g.integers(1, 12, 60) * ROWS + np.where(g.random(60) < 0.5, 0, g.integers(1, 127, 60))]
+    while len(tiles_of(requests(lengths, L), L)) > 225:
+        lengths.pop()
+    ids = requests(lengths, L, [(0, 1), (14, 15)])
+    kinds = tiles_of(ids, L)
+    assert expand_steps(kinds, N, R) >= {"TT", "TP", "PT", "TF", "FT", "FF"}
+    _, t = make(ids.size, N, K, R, L, 70 + R)
+    compare(fp8, ids, t, K, R, L)
