@@ -281,6 +281,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
         *reinterpret_cast<uint2*>(o) = hi;
         *reinterpret_cast<uint2*>(o + S::RP) = lo;
       }
+      // TMA may write the next item over the sums, which this thread wrote into
+      // its own ring and read from the others'
+      ptx::fence_proxy_async_cluster();
     }
     __syncwarp();
     ptx::cluster_sync();  // the ring is free again, here and for the others' reads

@@ -38,6 +38,13 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+// Plain reads and writes of any of the cluster's shared memory before this
+// fence come before what TMA does there after it (once a barrier has ordered
+// the two threads).
+__device__ __forceinline__ void fence_proxy_async_cluster() {
+  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+}
+
 // Global to shared, past L1; zeros when `in` is false (the address must be
 // valid all the same).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
