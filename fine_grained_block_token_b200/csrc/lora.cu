@@ -481,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, kRT <= 2 ? 2 : 1) lora_few_kernel(co
           __syncthreads();
           for (int i = threadIdx.x * 4; i < tile.rows * RP; i += kThreads * 4)
             *reinterpret_cast<float4*>(sums + i) = sum_warps<kRT>(part, i);
+          __syncwarp();
           ptx::cluster_sync();
           for (int i = threadIdx.x * 4; i < tile.rows * RP; i += kThreads * 4) {
             float4 v[kFew];

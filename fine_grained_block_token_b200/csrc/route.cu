@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
   }
   // One block, or one cluster whose blocks add up a share of the experts each
   // over all blocks, in order.
+  __syncwarp();
   ptx::cluster_sync();
   const uint32_t rank = ptx::cluster_ctarank();
   int rows = 0;
@@ -450,6 +451,7 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
     for (int w = 0; w < kWarps; ++w) t += red[w];
     st_cluster_double(&terms[rank], 0, t);
   }
+  __syncwarp();
   ptx::cluster_sync();  // also: the others have read this block's sums
   if (rank == 0 && threadIdx.x == 0 && want_share) {
     double t = 0.0;
@@ -472,6 +474,7 @@ __global__ void __launch_bounds__(kFinalThreads) route_final_kernel(const RouteA
   __shared__ int s_rows[kWarps];
   const int w = threadIdx.x / 32, l = threadIdx.x % 32;
   const uint32_t rank = ptx::cluster_ctarank();
+  __syncwarp();
   ptx::cluster_sync();  // block 0's shared memory may be written only once it runs
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
@@ -521,6 +524,7 @@ __global__ void __launch_bounds__(kFinalThreads) route_final_kernel(const RouteA
     for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(kFull, term, o);
     if (l == 0) st_cluster_double(&terms[rank], 0, term);
   }
+  __syncwarp();
   ptx::cluster_sync();
   if (rank == 0 && threadIdx.x == 0) {
     double t = 0.0;
