@@ -49,6 +49,13 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
+// The lanes of this thread's row, as bits of the warp.
+template <int kLanes>
+__device__ __forceinline__ unsigned lanes_of_row() {
+  if constexpr (kLanes == 32) return kFull;
+  return ((1u << (kLanes % 32)) - 1u) << (threadIdx.x % 32 / kLanes * kLanes);
+}
+
 // Largest of the lanes of a row (no NaN among them); a whole warp has an
 // instruction for it.
 template <int kLanes>
@@ -286,8 +293,7 @@ __global__ void __launch_bounds__(kForward<kVals>, 1) route_kernel(const RouteAr
 
   const int g = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
   const int lane = threadIdx.x % 32;
-  // the lanes of this row group, as bits of the warp
-  const unsigned group = kLanes == 32 ? kFull : ((1u << (kLanes % 32)) - 1u) << (lane - l);
+  const unsigned group = lanes_of_row<kLanes>();
   const int first = l * kVals, valid = a.E - first;
   float acc[kVals];
 #pragma unroll
@@ -559,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int g = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+  const unsigned group = lanes_of_row<kLanes>();
   const int first = l * kVals, valid = a.E - first;
   const float d_loss = a.loss_grad ? (a.d_loss ? *a.d_loss : 1.0f) : 0.0f;
   float up[kVals];
@@ -573,7 +580,17 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
     const T* zr = static_cast<const T*>(a.logits) + base;
     T* dr = static_cast<T*>(a.d_logits) + base;
     const int64_t slot0 = static_cast<int64_t>(row) * a.k;
-    const bool used = row < a.T && a.ids[slot0] >= 0;  // chose anything
+    // the chosen of this lane's slots, and whether the row has any
+    int id[kSlots];
+    bool any = false;
+#pragma unroll
+    for (int t = 0; t < kSlots; ++t) {
+      const int j = l + t * kLanes;
+      id[t] = row < a.T && j < a.k ? a.ids[slot0 + j] : -1;
+      if (id[t] < 0 || id[t] >= a.E) id[t] = -1;
+      any = any || id[t] >= 0;
+    }
+    const bool used = (__ballot_sync(kFull, any) & group) != 0;
     float z[kVals];
     if (used) {
       load_vals<T, kVals>(zr + first, valid, a.vec, z);
@@ -581,16 +598,13 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
 #pragma unroll
       for (int i = 0; i < kVals; ++i) z[i] = -INFINITY;
     }
-    // the chosen of this lane's slots, their logits on their way early
-    int id[kSlots];
+    // the chosen's logits on their way early
     float zc[kSlots], down[kSlots];
 #pragma unroll
     for (int t = 0; t < kSlots; ++t) {
-      const int j = l + t * kLanes;
-      id[t] = used && a.d_weights && j < a.k ? a.ids[slot0 + j] : -1;
-      if (id[t] >= a.E) id[t] = -1;
-      down[t] = id[t] >= 0 ? a.d_weights[slot0 + j] * a.scale : 0.0f;
-      zc[t] = id[t] >= 0 ? to_float(zr[id[t]]) : -INFINITY;
+      const bool in = a.d_weights && id[t] >= 0;
+      down[t] = in ? a.d_weights[slot0 + l + t * kLanes] * a.scale : 0.0f;
+      zc[t] = in ? to_float(zr[id[t]]) : -INFINITY;
     }
     float top = -INFINITY;
 #pragma unroll

@@ -66,7 +66,7 @@ def route_backward(logits, ids, d_weights=None, loss_grad=None, d_loss=1.0, scor
     d = np.zeros((T, E))
     for t in range(T):
         at = [int(i) for i in ids[t] if 0 <= i < E]
-        if not at or ids[t, 0] < 0:
+        if not at:
             continue
         slots = [j for j, i in enumerate(ids[t]) if 0 <= i < E]
         score, share = _scores(z[t], scoring)
