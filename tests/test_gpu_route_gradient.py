@@ -50,3 +50,65 @@ def test_ids_outside_the_experts_are_none(fp8, E, with_weights, renorm, scoring)
                               renorm, 2.0)
     mag = 2 * np.abs(np64(slope)).max() + (0 if dw is None else 8 * np.abs(np64(dw)).max())
     near(np64(d), want, 400 * U * mag, "d_logits")
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_same_bits_beside_any_number_of_closed_experts(fp8, dtype, renorm, scoring):
+    """Two open experts and any number of closed ones (-inf): weights and their
+    gradient are the same bits, whatever the width that serves the row.  (Sums
+    of two terms and zeros do not depend on their order.)"""
+    T = 400
+    z = logits_of(T, 2, dtype, 3).cuda()
+    dw = torch.randn(T, 2, generator=torch.Generator().manual_seed(4)).cuda()
+    first = None
+    for E in (2, 8, 9, 16, 17, 32, 33, 64, 65, 128, 200, 256, 257, 512, 600, 1024):
+        wide = torch.full((T, E), float("-inf"), dtype=dtype, device="cuda")
+        wide[:, :2] = z
+        ids, w, _, _, _ = fp8.route(wide, 2, scoring, renorm, 2.5)
+        d = fp8.route_backward(wide, ids, dw, None, None, scoring, renorm, 2.5)
+        assert (d[:, 2:] == 0).all()
+        got = ids, w, d[:, :2]
+        first = first or got
+        for a, b in zip(got, first):
+            assert torch.equal(a, b), E
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("E,k", [(8, 1), (8, 2), (16, 1), (16, 2), (17, 2), (32, 1), (64, 6), (100, 2), (256, 1), (256, 8),
+                                 (1000, 8)])
+def test_gradient_by_each_rows_own_terms(fp8, E, k, dtype, renorm, scoring):
+    """Tolerance from the terms of the row itself.  With A the largest |z - top| and
+    |z| of the row a score is off by e = (2.22 A + 8) u; a share, or a part of the
+    chosen scores, by two scores, up to 37 additions and a quotient,
+    s = 2 e + 40 u; a sum of shares times inputs by s + 37 u + 3 u of the sum of
+    magnitudes; 1 - s by e + 3 u.  Together below 3 s + 60 u of
+      f_e (q_e (|up_e| + sum q |up|) + r_e (|down_e| + sum r |down|))
+    with q the shares, r the scores that carry the weights' gradient (and, where
+    these are softmax shares themselves, q_e sum q |down|), f = 1 - s or 1."""
+    T, scale = 300, 2.5
+    z = logits_of(T, E, dtype, 11 * E + k)
+    zd, zz = z.cuda(), np64(z)
+    ids, _, _, _, slope = fp8.route(zd, k, scoring, renorm, scale, 0.1)
+    i0 = ids.cpu().numpy()
+    dw = torch.from_numpy(np.random.default_rng(k).standard_normal((T, k)).astype(np.float32))
+    d = fp8.route_backward(zd, ids, dw.cuda(), slope, None, scoring, renorm, scale)
+    fp8.check()
+    want = ref.route_backward(zz, i0, np64(dw), np64(slope), 1.0, scoring, renorm, scale)
+    up, down = np.abs(np64(slope)), scale * np.abs(np64(dw))
+    mag = np.zeros((T, E))
+    for t in range(T):
+        score, share = ref._scores(zz[t], scoring)
+        f = np.ones(E) if scoring == "softmax" else 1 - score
+        mag[t] = f * share * (up + (share * up).sum())
+        r = score[i0[t]] / score[i0[t]].sum() if renorm else score[i0[t]]
+        mag[t, i0[t]] += f[i0[t]] * r * (down[t] + (r * down[t]).sum())
+        if scoring == "softmax" and not renorm:
+            mag[t] += share * (score[i0[t]] * down[t]).sum()
+    A = np.maximum(np.abs(zz - zz.max(1, keepdims=True)), np.abs(zz)).max(1, keepdims=True)
+    s = (2 * (2.22 * A + 8) + 40) * U
+    half = HALF_BF16 if dtype == torch.bfloat16 else U
+    near(np64(d), want, (3 * s + 60 * U) * mag + half * np.abs(want) + 1e-38, "d_logits")
