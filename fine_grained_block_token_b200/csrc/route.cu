@@ -165,11 +165,12 @@ __device__ __forceinline__ float fast_rcp(float x) {
 
 // Scores of a row from its logits and its largest, `top`: e[i] is the score
 // times a factor common to the row (softmax: its denominator; sigmoid: 1, or
-// exp(-top) where every logit is below kFar and scores might underflow), so
-// e / sum is the share.  e is off by (2.22 |z - top| + 4) u of itself where the
+// exp(-top) where every logit is below kFar), so e / sum is the share.  Below
+// kFar 1 + exp(z) is 1 in fp32 and a score is exp(z): exp(z - top) keeps the
+// ratios of a row down to e^-87 where the scores themselves underflow.  e is off by (2.22 |z - top| + 4) u of itself where the
 // exponent is z - top (its own rounding comes in), and by (1.22 |z| + 7) u for a
 // sigmoid score (the sum with 1 and its reciprocal come in).
-constexpr float kFar = -60.0f;
+constexpr float kFar = -18.0f;
 
 template <int kLanes, int kVals, bool kSigmoid>
 struct RowScores {
@@ -178,7 +179,7 @@ struct RowScores {
 
   __device__ __forceinline__ float value(float z) const {
     if (kSigmoid && !far) return fast_rcp(1.0f + fast_exp(-z));
-    return fast_exp(z - shift);  // below kFar, 1 + exp(z) is 1
+    return fast_exp(z - shift);
   }
 
   __device__ __forceinline__ RowScores(float top, const float (&z)[kVals], float (&e)[kVals]) {

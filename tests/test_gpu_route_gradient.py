@@ -112,3 +112,32 @@ def test_gradient_by_each_rows_own_terms(fp8, E, k, dtype, renorm, scoring):
     s = (2 * (2.22 * A + 8) + 40) * U
     half = HALF_BF16 if dtype == torch.bfloat16 else U
     near(np64(d), want, (3 * s + 60 * U) * mag + half * np.abs(want) + 1e-38, "d_logits")
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E", [8, 64, 256])
+def test_sigmoid_rows_far_below_zero_keep_their_ratios(fp8, E, renorm):
+    """Rows whose scores lie on both sides of fp32's range, beside the top one:
+    renormalised weights are ratios and stay what they are (e^-40 = 4e-18), with
+    their gradient.  |z - top| <= 70: e is off by (2.22 * 70 + 8) u, a ratio by
+    twice that and 40 u, below 400 u; a score below 2^-126 may come out as any
+    value down to 0."""
+    tops = torch.tensor([-19.0, -25.0, -31.0, -40.0, -55.0, -59.5, -61.0, -80.0, -100.0])
+    T, k = tops.numel(), 4
+    z = torch.full((T, E), -300.0)
+    for j, below in enumerate((0.0, 12.5, 40.0, 66.0)):
+        z[:, 2 * j + 1] = tops - below
+    ids, w, _, _, _ = fp8.route(z.cuda(), k, "sigmoid", renorm, 2.5)
+    i0, w0, _, _, _ = ref.route(np64(z), k, "sigmoid", renorm, 2.5)
+    assert np.array_equal(ids.cpu().numpy(), i0)
+    near(np64(w), w0, 400 * U * w0 + (0 if renorm else 2.5 * 2.0 ** -126), "weights")
+    for j in range(k):
+        dw = torch.zeros(T, k)
+        dw[:, j] = 1.0
+        d = fp8.route_backward(z.cuda(), ids, dw.cuda(), None, None, "sigmoid", renorm, 2.5)
+        want = ref.route_backward(np64(z), i0, np64(dw), None, 1.0, "sigmoid", renorm, 2.5)
+        r = w0 / 2.5
+        mag = np.zeros((T, E))
+        np.put_along_axis(mag, i0, 2.5 * r * (np64(dw) + (r * np64(dw)).sum(1, keepdims=True)) if renorm
+                          else 2.5 * r * np64(dw), axis=1)
+        near(np64(d), want, 2 * 400 * U * mag + 2.5 * 2.0 ** -126, f"d_logits of {j}")
