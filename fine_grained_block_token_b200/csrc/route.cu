@@ -633,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
         part += v[t];
       }
       if (a.renorm) part = sum_lanes<kLanes>(part);
+      if (sc.sum != sc.sum) part = sc.sum;  // a NaN logit beside the chosen
 #pragma unroll
       for (int t = 0; t < kSlots; ++t) {
         if (a.renorm && id[t] >= 0) v[t] = __fdiv_rn(v[t], part);
@@ -640,6 +641,8 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
       }
       mix = sum_lanes<kLanes>(mix);
     }
+    // without a gradient through the shares a NaN logit reaches the chosen alone
+    const bool shares = a.loss_grad || (!kSigmoid && !a.renorm && a.d_weights);
     // softmax without renormalisation: every expert's score loses
     // p_e * sum_j p_j d_w_j; with it, the chosen share that among themselves
     const float all = dot + (!kSigmoid && !a.renorm ? mix * inv : 0.0f);
@@ -650,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
         float x = e[i] * (up[i] - all);
         // 1 - s = 1 / (1 + exp(z))
         if constexpr (kSigmoid) x *= fast_rcp(1.0f + fast_exp(z[i]));
-        d[i] = used ? x : 0.0f;
+        d[i] = used && shares ? x : 0.0f;
       }
       store_vals<T, kVals>(dr + first, valid, a.vec, d);
     }
@@ -661,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 1) route_backward_k
         if (id[t] < 0) continue;
         const float u = a.loss_grad ? a.loss_grad[id[t]] * d_loss : 0.0f;
         const float score = sc.value(zc[t]);
-        float dz = score * inv * (u - all);
+        float dz = shares ? score * inv * (u - all) : 0.0f;
         if (a.renorm)
           dz += v[t] * (down[t] - mix);
         else if (kSigmoid)

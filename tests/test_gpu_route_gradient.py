@@ -141,3 +141,27 @@ def test_sigmoid_rows_far_below_zero_keep_their_ratios(fp8, E, renorm):
         np.put_along_axis(mag, i0, 2.5 * r * (np64(dw) + (r * np64(dw)).sum(1, keepdims=True)) if renorm
                           else 2.5 * r * np64(dw), axis=1)
         near(np64(d), want, 2 * 400 * U * mag + 2.5 * 2.0 ** -126, f"d_logits of {j}")
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("with_loss", [True, False])
+@pytest.mark.parametrize("E", [8, 64, 256])
+def test_a_nan_logit_goes_where_the_formula_takes_it(fp8, E, with_loss, renorm, scoring):
+    """Beside chosen experts a NaN logit reaches the whole row through the shares;
+    without a gradient through them, what the chosen scores' sum reaches, and
+    with sigmoid scores on their own nothing."""
+    T, k = 12, 3
+    z = logits_of(T, E, torch.float32, 5)
+    z[2, 1] = float("nan")
+    z[7, E - 1] = float("nan")
+    zd = z.cuda()
+    ids, _, _, _, slope = fp8.route(zd, k, scoring, renorm, 2.0, 0.0)
+    dw = torch.from_numpy(np.random.default_rng(E).standard_normal((T, k)).astype(np.float32)).cuda()
+    up = torch.full((E,), 0.25, device="cuda") if with_loss else None
+    for d_weights in (dw, None):
+        d = fp8.route_backward(zd, ids, d_weights, up, None, scoring, renorm, 2.0)
+        want = ref.route_backward(np64(z), ids.cpu().numpy(), None if d_weights is None else np64(dw),
+                                  None if up is None else np64(up), 1.0, scoring, renorm, 2.0)
+        assert np.isnan(want).any() == (with_loss or d_weights is not None and (renorm or scoring == "softmax"))
+        near(np64(d), want, 400 * U * (0.5 + 8 * np.abs(np64(dw)).max()), "d_logits")
