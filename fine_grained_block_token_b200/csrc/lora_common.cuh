@@ -126,12 +126,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// a and b as the nearest bf16 pair and the bf16 pair nearest to the rest
-// (none beside an infinity or a NaN).
+// a and b as the nearest finite bf16 pair and the bf16 pair nearest to the rest:
+// fp32's last values above bf16's largest keep a finite rest, an infinity goes
+// into it whole.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16(a, b);
-  const float ra = a - lo_f(hi), rb = b - hi_f(hi);
-  lo = pack_bf16(ra == ra ? ra : 0.0f, rb == rb ? rb : 0.0f);
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+  lo = pack_bf16(a - lo_f(hi), b - hi_f(hi));
 }
 
 // y + c of two neighbouring columns, rounded once
