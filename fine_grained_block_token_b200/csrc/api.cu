@@ -609,7 +609,9 @@ fp8bl_status fp8bl_combine_rows_backward(const void* d_out_bf16, const void* y_b
 static bool lora_dims_ok(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
   return dim_ok(M, true) && dim_ok(N, false) && dim_ok(K, false) && N % 8 == 0 && K % 8 == 0 &&
          R >= 8 && R <= kMaxRank && R % 8 == 0 && L >= 1 && L <= kMaxExperts &&
-         L * N <= FP8BL_MAX_DIM;
+         L * N <= FP8BL_MAX_DIM &&
+         // tiles of 128 rows are counted in 32 bits, whatever the offsets hold
+         (L + 1) * M <= 128 * FP8BL_MAX_DIM;
 }
 
 size_t fp8bl_lora_add_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {

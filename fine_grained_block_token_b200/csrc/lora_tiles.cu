@@ -53,7 +53,7 @@ __device__ __forceinline__ uint32_t cell(int r, int c) {
 // in one piece), else -1.  Whole warp.
 __device__ __forceinline__ int first_of_run(const Args& p, const Tile& tile) {
   const int lane = threadIdx.x % 32, first = p.order[tile.pos];
-  bool run = first >= 0 && first + tile.rows <= p.M;
+  bool run = first >= 0 && first <= p.M - tile.rows;
 #pragma unroll
   for (int i = 0; i < kRows / 32; ++i) {
     const int r = i * 32 + lane;

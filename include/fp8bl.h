@@ -504,7 +504,7 @@ fp8bl_status fp8bl_combine_rows_backward(const void *d_out_bf16, const void *y_b
  *            (16-byte aligned), or NULL when that is 0; contents ignored.
  *   M >= 0 (M == 0 enqueues nothing), N, K > 0 and multiples of 8, R a
  *   multiple of 8 up to 128 (pad adapters of smaller rank with zeros),
- *   1 <= L <= 1024, L * N <= FP8BL_MAX_DIM.
+ *   1 <= L <= 1024, L * N <= FP8BL_MAX_DIM, (L + 1) * M <= 128 * FP8BL_MAX_DIM.
  */
 size_t fp8bl_lora_add_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L);
 fp8bl_status fp8bl_lora_add(const void *x_bf16, const void *a_bf16, const void *b_bf16,

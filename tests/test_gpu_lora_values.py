@@ -56,3 +56,21 @@ def test_infinite_inner_products(fp8, M, R):
     assert (row[cols] == float("inf")).all() and torch.isnan(row[5])
     keep = torch.arange(M) != M // 2
     assert torch.isfinite(got.cpu()[keep]).all()
+
+
+def test_an_order_past_the_last_integer(fp8):
+    """A full tile whose rows count on past 2^31 - 1: skipped, as all rows outside
+    [0, M) are."""
+    M, N, K, R = 1100, 64, 64, 8
+    ids, t = make(M, N, K, R, 1, 62, bare=0.0)
+    d = {k: v.cuda() for k, v in t.items()}
+    off, order, _ = fp8.group_rows(torch.zeros(M, dtype=torch.int32, device="cuda"), 1)
+    good = fp8.lora_add(d["y"], d["x"], d["a"], d["b"], off, order, scales=d["scales"])
+    far = order.clone()
+    far[256:384] = torch.from_numpy((2 ** 31 - 64 + np.arange(128)).astype(np.uint32).view(np.int32)).cuda()
+    out = torch.full_like(d["y"], 7.0)
+    fp8.lora_add(d["y"], d["x"], d["a"], d["b"], off, far, scales=d["scales"], out=out)
+    fp8.check()
+    keep = torch.ones(M, dtype=torch.bool)
+    keep[256:384] = False
+    assert torch.equal(out[keep], good[keep]) and (out[256:384] == 7.0).all()

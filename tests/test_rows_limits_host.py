@@ -1,0 +1,26 @@
+"""Host-side checks of the row calls' limits (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from tests.test_rows_host import AT, I64, SHAPE, SZ, V, _call
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from fine_grained_block_token_b200 import build
+    return ctypes.CDLL(build.build())
+
+
+def test_adapter_tiles_are_counted_in_32_bits(lib):
+    """Offsets that go up and down may name every row (L + 1) / 2 times over; the
+    tiles they make still have to be countable."""
+    def status(M, L):
+        return _call(lib.fp8bl_lora_add, [V] * 8 + [I64] * 5 + [V, SZ, V],
+                     [*AT[:8], M, 8, 8, 8, L, None, 0, None])
+    for M, L in ((1 << 30, 1024), (1 << 28, 1024), (1 << 30, 128)):
+        assert (L + 1) * M > 1 << 37 and status(M, L) == SHAPE
+    lib.fp8bl_lora_add_workspace_bytes.argtypes, lib.fp8bl_lora_add_workspace_bytes.restype = [I64] * 5, SZ
+    assert lib.fp8bl_lora_add_workspace_bytes(1 << 30, 8, 8, 8, 128) == 0
+    assert lib.fp8bl_lora_add_workspace_bytes(1 << 30, 8, 8, 8, 127) > 0
+    assert lib.fp8bl_lora_add_workspace_bytes(1 << 26, 8, 8, 8, 1024) > 0
