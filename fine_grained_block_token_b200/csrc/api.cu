@@ -81,7 +81,9 @@ const char* fp8bl_status_string(fp8bl_status s) {
   switch (s) {
     case FP8BL_OK: return "ok";
     case FP8BL_ERR_NULL: return "a required pointer is NULL";
-    case FP8BL_ERR_SHAPE: return "invalid sizes or options for this call (see its limits)";
+    case FP8BL_ERR_SHAPE:
+      return "invalid sizes or options (block-scaled linears need K, N multiples of 128; each call "
+             "states its limits)";
     case FP8BL_ERR_ALIGN: return "pointer not 16-byte aligned (4-byte for fp32 scales)";
     case FP8BL_ERR_ARCH: return "current device is not compute capability 10.0 (sm_100)";
     case FP8BL_ERR_CUDA: return "CUDA call failed";

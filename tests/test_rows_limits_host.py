@@ -24,3 +24,9 @@ def test_adapter_tiles_are_counted_in_32_bits(lib):
     assert lib.fp8bl_lora_add_workspace_bytes(1 << 30, 8, 8, 8, 128) == 0
     assert lib.fp8bl_lora_add_workspace_bytes(1 << 30, 8, 8, 8, 127) > 0
     assert lib.fp8bl_lora_add_workspace_bytes(1 << 26, 8, 8, 8, 1024) > 0
+
+
+def test_the_size_error_names_the_linears_multiple(lib):
+    """The most frequent wrong size of the linears stays in the message."""
+    lib.fp8bl_status_string.restype = ctypes.c_char_p
+    assert b"multiples of 128" in lib.fp8bl_status_string(SHAPE)
