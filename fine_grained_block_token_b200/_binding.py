@@ -397,6 +397,7 @@ def linear_rowwise(q_a, s_a, q_w, s_w, y=None) -> torch.Tensor:
 _I32 = (torch.int32,)
 _LOGITS = {torch.bfloat16: 0, torch.float32: 1}
 _SCORING = {"softmax": 0, "sigmoid": 1}
+_MAX_GROUPS, _MAX_TOP_K = 1024, 32
 
 
 def _out(t, name: str, dtype, shape, device) -> torch.Tensor:
@@ -407,6 +408,13 @@ def _out(t, name: str, dtype, shape, device) -> torch.Tensor:
             and t.is_contiguous()):
         _need(t, name, (dtype,), shape, device)
     return t
+
+
+def _count(v, most: int, where: str) -> None:
+    """A number that sizes outputs, refused as the library would before they are
+    allocated."""
+    if not 1 <= v <= most:
+        raise Fp8blError(2, where)
 
 
 def _scratch(given, device, size, *sizes):
@@ -447,6 +455,7 @@ def route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = True
     route_backward takes.  `mask` (bool [T]) leaves rows out.  Outputs and
     workspace (uint8, route_workspace_bytes(T, E)) may be given."""
     dev, T, E, kind, score = _route_options(logits, scoring)
+    _count(top_k, min(E, _MAX_TOP_K), "fp8bl_route")
     if mask is not None:
         _need(mask, "mask", (torch.bool, torch.uint8), (T,), dev)
     ids = _out(ids, "ids", torch.int32, (T, top_k), dev)
@@ -498,6 +507,7 @@ def group_rows(ids, groups: int, offsets=None, order=None, slot=None, workspace=
     dev = _device_of(ids, "ids")
     _need(ids, "ids", _I32, None, dev)
     n = ids.numel()
+    _count(groups, _MAX_GROUPS, "fp8bl_group_rows")
     offsets = _out(offsets, "offsets", torch.int32, (groups + 1,), dev)
     order = _out(order, "order", torch.int32, (n,), dev)
     slot = _out(slot, "slot", torch.int32, ids.shape, dev)
