@@ -150,8 +150,7 @@ __device__ __forceinline__ void store_vals(T* p, int valid, bool vec, const floa
 //   64          8.4e-8 and 8.4e-8 | 1.2e-7 and 9.8e-8
 //   256         8.1e-8 and 8.0e-8 | 1.3e-7 and 9.6e-8
 // (the same formulas in fp32 tensor operations: 0.7 to 0.9e-7 | 1.9e-7 to 2.5e-6),
-// and expf takes 19.2 | 20.1 us instead of 18.4 | 18.6 for 16384 x 256 and 10.3 | 11.2
-// instead of 9.5 | 10.0 for 4093 x 16.
+// and expf takes 19.2 | 20.1 us instead of 18.4 | 18.6 for 16384 x 256.
 __device__ __forceinline__ float fast_exp(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));  // log2(e)
@@ -699,16 +698,22 @@ cudaError_t by_type(bool f32, bool sigmoid, int64_t E, F f) {
   return sigmoid ? by_width<__nv_bfloat16, true>(E, f) : by_width<__nv_bfloat16, false>(E, f);
 }
 
-// Blocks of the forward kernel: one while its rows take up to two turns; then
-// one cluster, up to four turns, which adds up its blocks' sums itself; beyond
-// that up to one per SM, and a second launch for the sums.  (16 experts,
-// softmax: the cluster's four turns take 11.0 us on the GPU for 4093 rows, 33
-// blocks and the second launch 6.3 us for 4097, but that launch costs the host
-// 2.6 us more, and a call by itself is bound by the host.)
+// Blocks of the forward kernel, by the time on the GPU: one for the rows that
+// it takes in one turn; one cluster for those that it takes in one turn, whose
+// blocks add up their sums themselves; beyond, up to one per SM, and a second
+// launch for the sums.  us, fp32 sigmoid, at 16 | 64 | 256 | 1024 experts:
+//   one turn of a block     one block 4.4 | 8.1 | 6.8 | 11.9, a cluster 5.5 | 9.2 | 8.1 | 12.4
+//   one and a half          5.5 | 11.3 | 8.8 | 13.7 and 5.7 | 9.5 | 8.0 | 12.4
+//   one turn of a cluster   5.6 | 9.6 | 7.8 | 13.3
+//   one and a quarter       a cluster 7.1 | 14.5 | 10.7 | 15.9, the grid 5.2 | 9.3 | 7.6 | 15.1
+//   four turns              10.1 | 23.6 | 16.6 | 24.0 and 5.8 | 9.6 | 8.2 | 17.7
+// The second launch costs the host 2.4 us: calls back to back that the host
+// bounds take 12.2 instead of 9.8 where 16 experts' rows would fit a cluster's two to
+// four turns.
 int route_blocks(int64_t T, int64_t E, int sm_count) {
   const int64_t rows = E <= 64 ? 128 : E <= 128 ? 64 : E <= 256 ? 32 : E <= 512 ? 16 : 8;
-  if (T <= 2 * rows) return 1;
-  if (T <= 4 * kCluster * rows) return kCluster;
+  if (T <= rows) return 1;
+  if (T <= kCluster * rows) return kCluster;
   const int64_t b = (T + rows - 1) / rows;
   return static_cast<int>(b > sm_count ? sm_count : b);
 }

@@ -30,3 +30,14 @@ def test_the_size_error_names_the_linears_multiple(lib):
     """The most frequent wrong size of the linears stays in the message."""
     lib.fp8bl_status_string.restype = ctypes.c_char_p
     assert b"multiples of 128" in lib.fp8bl_status_string(SHAPE)
+
+
+@pytest.mark.parametrize("E,rows", [(8, 128), (16, 128), (64, 128), (100, 64), (256, 32), (512, 16), (1024, 8)])
+def test_the_router_takes_the_whole_gpu_beyond_one_turn_of_a_cluster(lib, E, rows):
+    """A block has `rows` rows in flight; what one cluster of eight cannot take at
+    once goes to all SMs, with a workspace for their sums."""
+    lib.fp8bl_route_workspace_bytes.argtypes, lib.fp8bl_route_workspace_bytes.restype = [I64] * 2, SZ
+    for T in (1, rows, rows + 1, 8 * rows):
+        assert lib.fp8bl_route_workspace_bytes(T, E) == 0
+    assert lib.fp8bl_route_workspace_bytes(8 * rows + 1, E) == 9 * (8 * E + 4)
+    assert lib.fp8bl_route_workspace_bytes(32 * rows, E) == 32 * (8 * E + 4)
