@@ -715,18 +715,22 @@ Plan plan_tiles(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, int sm_co
   const int64_t least = (M + kRows - 1) / kRows, most = M / kRows + (L + 1 < M ? L + 1 : M);
   // Blocks of a cluster: as many as keep the tiles that are likely (full ones
   // and a partial one for each adapter) resident at once, two blocks per SM,
-  // with at least 256 of K each.  Sizes between the powers of two pay where
-  // every block still has a long way through K (5003 rows, K = 14336: 6 in place
-  // of 4, 60 -> 57 us; 4096 rows, K = 4096: 7 in place of 4, 121 -> 126) and if the
-  // clusters fit the chip with a margin (47 tiles of 6: 63 -> 78).
-  const int64_t likely = least + (L < least ? L : least);
+  // with at least 256 of K each.  A cluster lies within one group of SMs, so of
+  // all blocks' places pairs can use all, clusters of 4 15/16 and others 5/6.
+  // Measured with every size at 28 to 150 tiles, K = 4096, 7168 and 14336, rank 16
+  // and 64, N = 4096: 8 blocks pay up to 32 tiles, 7 up to 36, 6 to 42, 5 to 49, 4 to
+  // 70, 3 to 85 and 2 to 148, at every K alike; the largest that fits is within 4% of the
+  // best, one that does not loses 10 to 25%.  us at rank 16, K = 4096 | 14336:
+  //   34 tiles   6 blocks 29 | 47     7 28 | 46     8 33 | 58
+  //   53         3 44 | 69            4 43 | 68     5 48 | 79
+  //   80         2 58 | 99            3 58 | 93     4 65 | 111
+  //   100        1 74 | 144           2 67 | 113    3 77 | 135
+  const int64_t likely = least + (L < least ? L : least), places = 2 * sm_count;
   p.max_splits = 1;
-  while (p.max_splits < 8 && likely * p.max_splits * 2 <= 2 * sm_count &&
-         K >= 512 * static_cast<int64_t>(p.max_splits))
-    p.max_splits *= 2;
-  const int64_t between = 2 * sm_count * 92 / 100 / likely;
-  if (between > p.max_splits && between <= 8 && K >= 1536 * between)
-    p.max_splits = static_cast<int>(between);
+  for (int s = 2; s <= 8; ++s) {
+    const int64_t fit = s == 2 ? places : s == 4 ? places * 15 / 16 : places * 5 / 6;
+    if (likely * s <= fit && K >= 256 * s) p.max_splits = s;
+  }
   const int64_t clusters = 2 * sm_count / p.max_splits;
   p.shrink_blocks = static_cast<int>((most < clusters ? most : clusters) * p.max_splits);
   const int64_t eb = most * ((N + kCols - 1) / kCols), er = sm_count * (p.rt == 8 ? 1 : 2);

@@ -89,21 +89,13 @@ def test_expand_goes_from_tile_to_tile(fp8, N, R):
     compare(fp8, ids, t, K, R, L)
 
 
-def shrink_steps(kinds, M, K, L):
-    """The steps from one tile to the next that the shrink's clusters take, and
-    the blocks of a cluster (sizes between the powers of two need a longer K)."""
-    assert K < 4608
-    sms = torch.cuda.get_device_properties(0).multi_processor_count
-    least = -(-M // ROWS)
-    likely, parts = least + min(L, least), 1
-    while parts < 8 and likely * parts * 2 <= 2 * sms and K >= 512 * parts:
-        parts *= 2
-    clusters = 2 * sms // parts
+def shrink_steps(kinds, clusters):
+    """The steps from one tile to the next that the shrink's clusters take."""
     steps = set()
     for c in range(clusters):
         mine = kinds[c::clusters]
         steps |= {a + b for a, b in zip(mine, mine[1:])}
-    return steps, parts
+    return steps
 
 
 @pytest.mark.parametrize("R", [8, 32, 64, 128])
@@ -116,26 +108,41 @@ def test_shrink_goes_from_tile_to_tile(fp8, K, R):
     lengths = [int(n) for n in g.integers(1, 30, 46) * ROWS + np.where(g.random(46) < 0.5, 0, g.integers(1, 127, 46))]
     ids = requests(lengths, L, [(0, 1), (9, 10), (25, 26), (30, 31)])
     kinds = tiles_of(ids, L)
-    steps, parts = shrink_steps(kinds, ids.size, K, L)
-    assert parts == 1 and steps >= {"TT", "TF", "FT", "FF", "TP", "PT"}
+    # too many for clusters of more than one block: two blocks per SM
+    clusters = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    assert shrink_steps(kinds, clusters) >= {"TT", "TF", "FT", "FF", "TP", "PT"}
     _, t = make(ids.size, N, K, R, L, 80 + R)
     compare(fp8, ids, t, K, R, L)
 
 
 @pytest.mark.parametrize("R", [8, 64, 128])
-@pytest.mark.parametrize("M,K,clusters", [(7680, 520, 148), (4000, 1160, 74), (2100, 2056, 37)])
-def test_shrink_clusters_go_from_tile_to_tile(fp8, M, K, clusters, R):
-    """The same where the blocks of a cluster share K: the ring also held what
-    the other blocks read.  Adapters with a few rows lie between two of long
-    requests, so that every cluster goes from the first to the second."""
+@pytest.mark.parametrize("M,K,parts", [(7680, 520, 2), (4000, 1160, 4), (2100, 1560, 6)])
+def test_shrink_clusters_go_from_tile_to_tile(fp8, M, K, parts, R):
+    """The same where the blocks of a cluster share K, at least 256 each: the ring
+    also held what the other blocks read.  Adapters with a few rows lie between
+    two of long requests, so that whatever number of clusters the chip holds
+    some go from the first to the second."""
     N, L = 72, 400
+    at_once = 2 * torch.cuda.get_device_properties(0).multi_processor_count // parts
     first, last = M * 3 // 8 // ROWS * ROWS, M // 4 // ROWS * ROWS
-    few = clusters - first // ROWS
+    few = at_once * 7 // 8 - 1
     ids = np.zeros(M, np.int32)
     ids[first:M - last] = 1 + np.arange(M - first - last) % few
     ids[M - last:] = L - 1
     kinds = tiles_of(ids, L)
-    steps, parts = shrink_steps(kinds, M, K, L)
-    assert parts > 1 and "TT" in steps
+    assert K // 256 == parts and len(kinds) > at_once
+    for clusters in range(at_once * 7 // 8, at_once + 1):
+        assert "TT" in shrink_steps(kinds, clusters)
     _, t = make(M, N, K, R, L, 90 + R)
     compare(fp8, ids, t, K, R, L)
+
+
+@pytest.mark.parametrize("R", [16, 72])
+@pytest.mark.parametrize("parts", range(1, 9))
+def test_clusters_of_every_size(fp8, parts, R):
+    """One part of K, at least 256 deep, for every block of a cluster: 1 to 8 blocks,
+    all of whose shares of the rows are added up, the last one's shorter too."""
+    M, N, K, L = 2100, 136, 256 * parts + 200, 3
+    ids, t = make(M, N, K, R, L, 100 + parts)
+    ids[:700] = 1
+    compare(fp8, ids.numpy(), t, K, R, L)
