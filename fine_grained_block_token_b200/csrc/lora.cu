@@ -5,15 +5,16 @@
 // have no adapter and keep y.
 //
 // Two kernels (for a few rows one): the shrink u = x A^T (K is long, R short)
-// and the expand out = y + s u B^T (N is long), both bound by memory.  This file holds the
-// form for batches of a few rows per adapter (decode): tiles of 16 rows, one
-// mma.m16n8k16 fragment high (the tensor core proper multiplies 64 or 128 rows
-// at a time; 16 rows leave it nothing to gain while B streams by).  A warp takes its operands from global memory
-// straight into registers in the fragment layout: the sum over k (or r) may
-// be taken in any order, so lane q of a row group owns 8 neighbouring k of
-// every 32 and reads them with one 16-byte load, for both operands alike; and
-// the columns of B are dealt to the n index so that a lane ends up with 8
-// neighbouring outputs.  Nothing is staged in shared memory.
+// and the expand out = y + s u B^T (N is long), both bound by memory.  This
+// file holds the form for batches of a few rows per adapter (decode): tiles of
+// 16 rows, one mma.m16n8k16 fragment high (the tensor core proper multiplies 64
+// or 128 rows at a time; 16 rows leave it nothing to gain while B streams by).
+// A warp takes its operands from global memory straight into registers in the
+// fragment layout: the sum over k (or r) may be taken in any order, so lane q
+// of a row group owns 8 neighbouring k of every 32 and reads them with one
+// 16-byte load, for both operands alike; and the columns of B are dealt to the
+// n index so that a lane ends up with 8 neighbouring outputs.  Nothing is
+// staged in shared memory.
 //
 // The adapters' matrices are what has to be read, so the work is dealt to
 // the whole GPU whatever the number of tiles: the shrink splits K into as
@@ -22,9 +23,10 @@
 // (programmatic dependent launch): it finds its tile and loads B and y ahead,
 // and only then waits for u.
 //
-// Beside 28672 x 4096 at rank 16: 64 rows of 48 adapters 19 us (58 MB, 46% of the
-// copy rate; the run of B itself goes at 7 TB/s, the rest is the chain launch -
-// offsets - x - u that precedes it), one row beside 4096 x 4096 5.7 us.
+// Beside 28672 x 4096 at rank 16: 64 rows of 48 adapters (58 MB) 17 us where the
+// adapters are in L2 from the call before, 27 where they come from memory: the
+// chain launch - offsets - x - u precedes all but the first steps of B.  One row
+// beside 4096 x 4096 5.1 us.
 //
 // u stays in fp32 between the two; the expand splits it into the bf16 nearest
 // to it and the bf16 nearest to the rest (16 significant bits together) and
@@ -86,8 +88,9 @@ constexpr int kSmallM = 2048;
 
 // Whether both products run in one launch.  On the GPU it takes as long as two,
 // us beside 28672 x 4096: rank 16, 1 row 6.0 | 5.8, 16 rows of 16 adapters 10.7 |
-// 11.1, and saves the host 2 (one row beside 4096 x 4096: 12.8 -> 10.5 a call); at larger ranks the cluster's 64 warps are too
-// few for B: rank 64, 1 row 7.4 | 8.3, but 2 rows 13.5 | 9.8, 16 rows 17 | 12.
+// 11.1, and saves the host 2 (one row beside 4096 x 4096: 12.8 -> 10.5 a call);
+// at larger ranks the cluster's 64 warps are too few for B: rank 64, 1 row 7.4 |
+// 8.3, but 2 rows 13.5 | 9.8, 16 rows 17 | 12.
 bool few_rows(int64_t M, int64_t R) { return M == 1 || (M <= kRows && R <= 16); }
 
 // Whether a batch goes through this form or through the 128-row tiles of
@@ -307,8 +310,8 @@ __device__ __forceinline__ void expand_run(const Args& p, const Tile& tile, cons
   for (int d = 0; d < kDepth; ++d)
     if (d < n) load(buf[d], d, d);
 
-  // u of the tile's rows.  Lane (g, q) holds, per 32 ranks, the 8 from 8 q on (with 16 ranks the 4 from 4 q
-  // on) of rows g and g + 8.
+  // u of the tile's rows.  Lane (g, q) holds, per 32 ranks, the 8 from 8 q on
+  // (with 16 ranks the 4 from 4 q on) of rows g and g + 8.
   before_u();
   uint32_t hi[kRT][4], lo[kRT][4];
   const float scale = p.scales ? p.scales[tile.group] : 1.0f;

@@ -8,9 +8,9 @@
 // of 128 threads from wherever `order` says; one thread issues the MMAs.  K is
 // split over the blocks of a cluster so that all SMs have work; the blocks'
 // sums meet through distributed shared memory, added in the order of the parts,
-// and leave as two bf16 terms side by side ([hi | lo], 2 RP deep).  (Parts that the expand adds up instead cost 38 of 137 us beside
-// 28672 x 4096 at rank 64 and 4096 rows: every block of the expand read all
-// seven.)
+// and leave as two bf16 terms side by side ([hi | lo], 2 RP deep).  (Parts that
+// the expand adds up instead cost 38 of 137 us beside 28672 x 4096 at rank 64
+// and 4096 rows: every block of the expand read all seven.)
 //
 // Expand, out = y + s u B^T: bound by reading y and writing out.  One
 // accumulation over hi and lo with B read twice multiplies by all 16 bits of
@@ -22,10 +22,12 @@
 // row piece), the accumulator added row by row (a thread per row, as tensor
 // memory hands it out) and written back, and out again the same way.
 //
-// 4096 rows of 8 adapters of rank 64 beside 28672 x 4096: 112 to 120 us for
-// 537 MB (73 to 68% of the copy rate): about 15 us of shrink, then 5.5 TB/s of y
-// and out, whose row pieces of 128 bytes lie N apart.  5003 rows at rank 16 beside
-// 4096 x 14336: 57 us for 227 MB, of which the shrink reads 142 MB in 27.
+// 4096 rows of 8 adapters of rank 64 beside 28672 x 4096: 109 to 121 us by how
+// the rows fall to the adapters, for 537 MB (75 to 68% of the copy rate): about 15
+// us of shrink, then 5.5 TB/s of y and out, whose row pieces of 128 bytes lie N
+// apart.  5003 rows at rank 16 beside 4096 x 14336: 56 to 58 us for 227 MB.  Alone
+// and from memory its shrink takes 37 us for 145 MB and its expand 26 for 82: ten
+// chunks a block are mostly the way in and out (DRAM 21%, issue 33%).
 //
 // Every wait is bounded; a thread whose wait ran out records the error, stops
 // waiting and runs its loops out (the barriers between threads still match).

@@ -22,8 +22,11 @@
 //
 // What bounds it is the instructions of the choice, not the bytes: with 256
 // experts a row costs about 580 warp instructions, 340 of them apart from the k
-// rounds.  16384 x 256 fp32 logits with 8 of 256: 15 us forward (17 MB), 4 us
-// for the sums of the blocks, 11 us for the gradient; one row: 5.4 us.
+// rounds.  16384 x 256 fp32 logits with 8 of 256: 15 us forward (17 MB, 61% of
+// the issue slots), 4 us for the sums of the blocks, 11 us for the gradient (half
+// the issue slots; what stalls it first are the loads of the chosen's logits and
+// slopes).  One row: 5.8 us, a block of 1024 threads and its sums for one warp's
+// work.
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -166,9 +169,10 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // times a factor common to the row (softmax: its denominator; sigmoid: 1, or
 // exp(-top) where every logit is below kFar), so e / sum is the share.  Below
 // kFar 1 + exp(z) is 1 in fp32 and a score is exp(z): exp(z - top) keeps the
-// ratios of a row down to e^-87 where the scores themselves underflow.  e is off by (2.22 |z - top| + 4) u of itself where the
-// exponent is z - top (its own rounding comes in), and by (1.22 |z| + 7) u for a
-// sigmoid score (the sum with 1 and its reciprocal come in).
+// ratios of a row down to e^-87 where the scores themselves underflow.  e is off
+// by (2.22 |z - top| + 4) u of itself where the exponent is z - top (its own
+// rounding comes in), and by (1.22 |z| + 7) u for a sigmoid score (the sum with 1
+// and its reciprocal come in).
 constexpr float kFar = -18.0f;
 
 template <int kLanes, int kVals, bool kSigmoid>
@@ -232,7 +236,6 @@ struct RouteArgs {
   int renorm, vec;
   float scale, balance;
 };
-
 
 __device__ __forceinline__ double loss_slope(float balance, int E, int k, int rows) {
   const double n = rows > 0 ? rows : 1;

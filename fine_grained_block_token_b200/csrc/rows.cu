@@ -42,7 +42,9 @@ cudaError_t launch_pdl(Kernel k, int64_t blocks, int threads, size_t smem, cudaS
 //
 // Bound by latency, not bytes: one launch up to 2048 entries (64 entries: 3 us
 // on the GPU), two beyond (131072 entries into 256 groups: 10 us, of which the
-// counts of 64 blocks per key and the scattered order are 5).
+// counts of 64 blocks per key and the scattered order are 5).  Beyond 131072 a
+// block takes its pieces one after another, 1.7 us each: 524288 entries 20 us,
+// 2097152 58.
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
